@@ -449,6 +449,120 @@ slstm_status slstm_head_backward_varlen(const void* P, slstm_dtype P_dtype, cons
                                         void* stream);
 
 /*
+ * Layer norm over the last axis of x (rows, width), dense: with mean and rstd = 1 / sqrt(var + eps)
+ * of each row (var the mean squared distance from the mean),
+ *   y = (x - mean) rstd weight + bias.
+ *  x, y        float32 or bf16 each (x_dtype, y_dtype: a float32 residual stream gives the bf16 x
+ *              of slstm_input_projection); aligned to their element
+ *  weight, bias (width) float32, NULL for 1 and 0;  eps >= 0, finite
+ *  mean, rstd  (rows) float32 outputs, NULL skips them (the backward takes both)
+ * rows >= 0 (0: nothing is done), 1 <= width <= 1048576. Statistics are float32.
+ */
+slstm_status slstm_layer_norm_forward(const void* x, slstm_dtype x_dtype, const float* weight,
+                                      const float* bias, float eps, void* y, slstm_dtype y_dtype,
+                                      float* mean, float* rstd, int64_t rows, int width, void* stream);
+
+/* Workspace bytes of slstm_layer_norm_backward with dweight or dbias (0 if invalid). */
+size_t slstm_layer_norm_backward_workspace_bytes(int64_t rows, int width);
+
+/*
+ * Gradients of the layer norm: with xh = (x - mean) rstd, g the gradient of y and gw = g weight,
+ *   dx = rstd (gw - mean(gw) - xh mean(gw xh)),  dweight = sum over rows of g xh,
+ *   dbias = sum over rows of g.
+ *  x, mean, rstd, weight as in the forward; g_y in g_dtype (float32 or bf16); dx in x's type.
+ *  dweight, dbias (width) float32, NULL skips them; without both no workspace is needed (NULL).
+ * The sums over rows are added in a fixed order: results are bitwise reproducible.
+ */
+slstm_status slstm_layer_norm_backward(const void* x, slstm_dtype x_dtype, const void* g_y,
+                                       slstm_dtype g_dtype, const float* mean, const float* rstd,
+                                       const float* weight, void* dx, float* dweight, float* dbias,
+                                       int64_t rows, int width, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/* A (B, T, n_heads, width) tensor in any order of its first three axes: element (b, t, h, i) is at
+ * data + b stride_b + t stride_t + h stride_h + i, in elements. data and strides are multiples of
+ * 16 bytes, strides >= 0 (0: shared along that axis; not in outputs), stride_t below 2^24. */
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_t, stride_h;
+} slstm_heads;
+
+/* Workspace bytes of slstm_linear_attention_forward (0 if invalid). n_seqs: the packed sequences,
+ * 0 for unpacked calls. */
+size_t slstm_linear_attention_workspace_bytes(int B, int T, int n_heads, int d_key, int d_value,
+                                              int n_seqs);
+
+/*
+ * Linear attention with a decay for each head (a matrix memory): per sequence and head, with a
+ * state S (d_key, d_value) and a log decay g_t,
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,   S_0 = state0 (NULL: zeros).
+ *  q, k (B, T, n_heads, d_key), v and out (B, T, n_heads, d_value): float32 or bf16, all of dtype.
+ *              d_key and d_value multiples of 8 up to 256; the three slices of a projection output
+ *              (B, T, 4, d_h) are such tensors.
+ *  log_decay   float32, (B, T, n_heads) dense, or (n_heads) with decay_per_head != 0: fixed for
+ *              all steps. At or below -104 (as -infinity) the decay is exactly 0: S_t = k_t v_t^T.
+ *  state0, final_state (B, n_heads, d_key, d_value) float32 dense, 16-byte aligned; NULL: zeros, and
+ *              not wanted. Both may be the same buffer.
+ *  cu_seqlens, n_seqs: packed sequences as in the _varlen calls (B = 1; states then per sequence;
+ *              an empty sequence passes its state0 on), NULL and 0 for unpacked calls.
+ * T >= 0 (0: final_state = state0). Steps are taken in chunks of 32 on the matrix cores and, where
+ * sequences and heads are too few for the GPU, in segments of the time axis that are joined. The
+ * state and every sum are float32. Results are bitwise reproducible. A step's output depends on
+ * that step and the ones before it only, also where later ones hold infinities or NaN.
+ * The workspace holds the segments' states (NULL if slstm_linear_attention_workspace_bytes is 0).
+ */
+slstm_status slstm_linear_attention_forward(const slstm_heads* q, const slstm_heads* k,
+                                            const slstm_heads* v, slstm_dtype dtype,
+                                            const float* log_decay, int decay_per_head,
+                                            const float* state0, float scale, const slstm_heads* out,
+                                            float* final_state, int B, int T, int n_heads, int d_key,
+                                            int d_value, const int* cu_seqlens, int n_seqs,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One step of the same recurrence (decoding), the states updated in place.
+ *  q, k (B, n_heads, d_key), v (B, n_heads, d_value): stride_t is not read; out (B, n_heads,
+ *              d_value) dense, of dtype.  log_decay (B, n_heads), or (n_heads) with decay_per_head.
+ *  state       (n_slots, n_heads, d_key, d_value) float32, 16-byte aligned: a pool of states
+ *  slots       (B) device int32: the state of each batch row; NULL: row b uses state b (n_slots >= B).
+ *              A row whose slot is outside 0 .. n_slots - 1 leaves the pool alone and outputs zeros.
+ *              Two rows of one call must not name the same slot.
+ */
+slstm_status slstm_linear_attention_step(const slstm_heads* q, const slstm_heads* k,
+                                         const slstm_heads* v, slstm_dtype dtype,
+                                         const float* log_decay, int decay_per_head, float* state,
+                                         const int* slots, int n_slots, float scale, void* out, int B,
+                                         int n_heads, int d_key, int d_value, void* stream);
+
+/* Workspace bytes of slstm_linear_attention_backward (0 if invalid). */
+size_t slstm_linear_attention_backward_workspace_bytes(int B, int T, int n_heads, int d_key,
+                                                       int d_value, int n_seqs);
+
+/*
+ * Gradients of slstm_linear_attention_forward, recomputed from its inputs: with L_t the gradient
+ * of S_t (L_T = g_final + scale q_T g_T^T, L_t = exp(g_{t+1}) L_{t+1} + scale q_t g_t^T),
+ *   dq_t = scale S_t g_t,  dk_t = L_t v_t,  dv_t = L_t^T k_t,  dstate0 = exp(g_1) L_1,
+ *   dlog_decay_t = <L_t, exp(g_t) S_{t-1}>   (0 where the decay is 0).
+ *  g_out       the gradient of out, of dtype; g_final that of final_state, NULL: zeros
+ *  dq, dk, dv  outputs of dtype (views: they may be slices of one tensor)
+ *  dlog_decay  (B, T, n_heads) float32, NULL skips it; refused with decay_per_head (a fixed decay
+ *              is not trained)
+ *  dstate0     as state0, NULL skips it
+ * With dlog_decay the products keep float32 precision (it is a sum whose terms cancel), without it
+ * that of the bf16 outputs. The workspace is always needed.
+ */
+slstm_status slstm_linear_attention_backward(const slstm_heads* q, const slstm_heads* k,
+                                             const slstm_heads* v, slstm_dtype dtype,
+                                             const float* log_decay, int decay_per_head,
+                                             const float* state0, float scale, const slstm_heads* g_out,
+                                             const float* g_final, const slstm_heads* dq,
+                                             const slstm_heads* dk, const slstm_heads* dv,
+                                             float* dlog_decay, float* dstate0, int B, int T,
+                                             int n_heads, int d_key, int d_value,
+                                             const int* cu_seqlens, int n_seqs, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+
+/*
  * Kernel timing with HIP events recorded on the launching stream around every kernel the
  * library launches, for measurement. Off by default; process-wide; not thread-safe.
  * slstm_profile_read waits for the recorded events and returns the summed duration (ms) and
@@ -471,7 +585,10 @@ typedef enum {
   SLSTM_KERNEL_HEAD_SEQUENTIAL = 13, /* the sequential forward under head mixing */
   SLSTM_KERNEL_HEAD_SOLVE = 14,      /* the whole Newton solve under head mixing, one sweep */
   SLSTM_KERNEL_HEAD_BACKWARD = 15,   /* the backward under head mixing (recurrence and sums) */
-  SLSTM_KERNEL_KINDS = 16
+  SLSTM_KERNEL_LAYER_NORM = 16,      /* layer norm, forward and backward (with its sums) */
+  SLSTM_KERNEL_LINEAR_ATTENTION = 17, /* linear attention: a forward or backward call's kernels */
+  SLSTM_KERNEL_LINEAR_STEP = 18,     /* linear attention: a single step */
+  SLSTM_KERNEL_KINDS = 19
 } slstm_kernel_kind;
 
 slstm_status slstm_profile_enable(int on);

@@ -11,6 +11,7 @@
 #include <cstring>
 #include <mutex>
 #include <random>
+#include <utility>
 #include <vector>
 
 #include "../../include/slstm.h"
@@ -1237,6 +1238,309 @@ slstm_status slstm_head_backward_varlen(const void* P, slstm_dtype P_dtype, cons
   if (s != SLSTM_OK) return s;
   return head_backward(P, P_dtype, R, state0, states, g_states, g_h, g_final, dP, dP_dtype, dR, dbias, dstate0, 1, T,
                        d_h, n_heads, fmode, workspace, workspace_bytes, stream, seqs);
+}
+
+}  // extern "C"
+
+namespace {
+
+bool known_dtype(slstm_dtype t) { return t == SLSTM_F32 || t == SLSTM_BF16; }
+
+size_t elem_size(slstm_dtype t) { return t == SLSTM_F32 ? 4 : 2; }
+
+constexpr int kMaxNormWidth = 1 << 20;
+
+slstm_status check_norm(int64_t rows, int width) {
+  if (rows < 0 || width < 1 || width > kMaxNormWidth)
+    return fail(SLSTM_EINVAL, "rows >= 0 and 1 <= width <= %d required (got %lld, %d)", kMaxNormWidth,
+                static_cast<long long>(rows), width);
+  if (rows > (int64_t{1} << 50) / width) return fail(SLSTM_EINVAL, "sizes too large");
+  return SLSTM_OK;
+}
+
+// ---- linear attention ----
+constexpr int kLinMaxWidth = 256;
+
+slstm_status check_linear(int B, int T, int H, int dk, int dv, int n_seqs) {
+  if (B < 1 || T < 0 || H < 1) return fail(SLSTM_EINVAL, "B, n_heads >= 1 and T >= 0 required (got %d, %d, %d)", B, H, T);
+  if (B > (1 << 24) || T > (1 << 24) || H > 65535)
+    return fail(SLSTM_EINVAL, "B, T <= 2^24 and n_heads <= 65535 required (got %d, %d, %d)", B, T, H);
+  if (dk < 8 || dk > kLinMaxWidth || dk % 8 != 0 || dv < 8 || dv > kLinMaxWidth || dv % 8 != 0)
+    return fail(SLSTM_EINVAL, "d_key and d_value must be multiples of 8 in 8..%d (got %d, %d)", kLinMaxWidth, dk, dv);
+  if (n_seqs < 0 || n_seqs > (1 << 24) || (n_seqs > 0 && B != 1))
+    return fail(SLSTM_EINVAL, "packed sequences take B = 1 and 1..2^24 sequences (got B = %d, %d)", B, n_seqs);
+  return SLSTM_OK;
+}
+
+slstm_status check_heads_view(const slstm_heads* v, const char* name, slstm_dtype t, bool empty) {
+  if (v == nullptr || (v->data == nullptr && !empty)) return fail(SLSTM_EINVAL, "%s must not be NULL", name);
+  const int64_t unit = static_cast<int64_t>(16 / elem_size(t));
+  if (!aligned(v->data, 16) || v->stride_b % unit != 0 || v->stride_t % unit != 0 || v->stride_h % unit != 0)
+    return fail(SLSTM_EINVAL, "%s and its strides must be multiples of 16 bytes", name);
+  if (v->stride_b < 0 || v->stride_t < 0 || v->stride_h < 0 || v->stride_t >= (1 << 24))
+    return fail(SLSTM_EINVAL, "%s: strides must be >= 0 and stride_t below 2^24", name);
+  return SLSTM_OK;
+}
+
+slstm::LinView view_of(const slstm_heads* v) { return {v->data, v->stride_b, v->stride_t, v->stride_h}; }
+
+// Segments of the time axis: as many as give every compute unit kLinWgsPerCu workgroups, none
+// shorter than kLinMinSeg steps. One segment needs no pass over k and v before the outputs.
+constexpr int kLinWgsPerCu = 2;
+constexpr int kLinMinSeg = 128;
+
+struct LinPlan {
+  int seg_len, n_seg, n_slots;
+  size_t states, decays, r, c, edge, total;  // offsets; states and decays per role
+  size_t state_bytes, decay_bytes;
+};
+
+LinPlan linear_plan(int B, int T, int H, int dk, int dv, int n_seqs, int roles) {
+  LinPlan p;
+  const i64 seqs = n_seqs > 0 ? n_seqs : B;
+  const i64 want = static_cast<i64>(kLinWgsPerCu) * device_cus();
+  const i64 have = seqs * H * roles;
+  i64 n = std::max<i64>(1, (want + have - 1) / have);
+  // packed: sequences of unknown lengths, of which T / seqs is the mean
+  const i64 mean = n_seqs > 0 ? std::max<i64>(1, T / seqs) : T;
+  i64 len = (mean + n - 1) / n;
+  len = std::max<i64>(kLinMinSeg, (len + 31) / 32 * 32);
+  if (n == 1 && n_seqs > 0) len = std::max<i64>(len, 4 * ((mean + 31) / 32 * 32));
+  if (n == 1 && n_seqs == 0) len = std::max<i64>(32, (static_cast<i64>(T) + 31) / 32 * 32);
+  p.seg_len = static_cast<int>(len);
+  p.n_seg = static_cast<int>(std::max<i64>(1, (T + len - 1) / len));
+  const i64 slots = n_seqs > 0 ? T / len + seqs : seqs * p.n_seg;
+  p.n_slots = static_cast<int>(std::min<i64>(slots, 0x7fffffff));
+  const bool split = p.n_seg > 1;
+  p.state_bytes = split ? align_up(static_cast<size_t>(slots) * H * dk * dv * sizeof(float)) : 0;
+  p.decay_bytes = split ? align_up(static_cast<size_t>(slots) * H * sizeof(float)) : 0;
+  p.states = 0;
+  p.decays = p.states + roles * p.state_bytes;
+  p.r = p.decays + roles * p.decay_bytes;
+  const size_t steps = roles > 1 ? align_up(static_cast<size_t>(B) * T * H * sizeof(float)) : 0;
+  p.c = p.r + steps;
+  p.edge = p.c + steps;
+  p.total = p.edge + (roles > 1 ? align_up(static_cast<size_t>(seqs) * H * sizeof(float)) : 0);
+  return p;
+}
+
+// walks of every role: the segments' states, their join, the outputs
+hipError_t linear_run(slstm::LinLaunch& a, const LinPlan& p, bool bf16, slstm::LinPass pass, void* workspace, hipStream_t st) {
+  a.seg_len = p.seg_len;
+  a.n_seg = p.n_seg;
+  a.n_slots = p.n_slots;
+  if (p.n_seg > 1) {
+    for (int i = 0; i < a.n_roles; ++i) {
+      a.role[i].seg_states = at<float>(workspace, p.states + i * p.state_bytes);
+      a.role[i].seg_decays = at<float>(workspace, p.decays + i * p.decay_bytes);
+    }
+    HIP_RET(slstm::launch_linear_walk(bf16, a, slstm::LinPass::kStates, st));
+    HIP_RET(slstm::launch_linear_join(a, st));
+  }
+  return slstm::launch_linear_walk(bf16, a, pass, st);
+}
+
+slstm_status check_linear_common(const slstm_heads* q, const slstm_heads* k, const slstm_heads* v, slstm_dtype dtype,
+                                 const float* log_decay, const float* state0, float scale, int B, int T, int H, int dk,
+                                 int dv, const int* cu, int n_seqs) {
+  slstm_status s = check_linear(B, T, H, dk, dv, n_seqs);
+  if (s != SLSTM_OK) return s;
+  if (!known_dtype(dtype)) return fail(SLSTM_EINVAL, "unknown dtype %d", (int)dtype);
+  if ((cu != nullptr) != (n_seqs > 0) || !aligned(cu, 4))
+    return fail(SLSTM_EINVAL, "cu_seqlens (4-byte aligned) and n_seqs >= 1 go together");
+  const bool empty = T == 0;
+  for (auto& x : {std::make_pair(q, "q"), std::make_pair(k, "k"), std::make_pair(v, "v")}) {
+    s = check_heads_view(x.first, x.second, dtype, empty);
+    if (s != SLSTM_OK) return s;
+  }
+  if ((log_decay == nullptr && !empty) || !aligned(log_decay, 4)) return fail(SLSTM_EINVAL, "log_decay must not be NULL, and 4-byte aligned");
+  if (!aligned(state0, 16)) return fail(SLSTM_EINVAL, "state0 must be 16-byte aligned");
+  if (!std::isfinite(scale)) return fail(SLSTM_EINVAL, "scale must be finite");
+  return SLSTM_OK;
+}
+
+slstm_status check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (need == 0) return SLSTM_OK;
+  if (workspace == nullptr || !aligned(workspace, kAlign)) return fail(SLSTM_EINVAL, "workspace must be non-NULL and 256-byte aligned");
+  if (bytes < need) return fail(SLSTM_EWORKSPACE, "workspace of %zu bytes, %zu needed", bytes, need);
+  return SLSTM_OK;
+}
+
+void linear_base(slstm::LinLaunch& a, const float* log_decay, int per_head, int B, int T, int H, const int* cu, int n_seqs) {
+  a.gate = log_decay;
+  a.gate_h = 1;
+  a.gate_t = per_head ? 0 : H;
+  a.gate_b = per_head ? 0 : static_cast<i64>(T) * H;
+  a.cu = cu;
+  a.n_seqs = n_seqs > 0 ? n_seqs : B;
+  a.T = T;
+  a.H = H;
+}
+
+}  // namespace
+
+extern "C" {
+
+slstm_status slstm_layer_norm_forward(const void* x, slstm_dtype x_dtype, const float* weight, const float* bias,
+                                      float eps, void* y, slstm_dtype y_dtype, float* mean, float* rstd,
+                                      int64_t rows, int width, void* stream) {
+  g_err[0] = '\0';
+  slstm_status s = check_norm(rows, width);
+  if (s != SLSTM_OK) return s;
+  if (!known_dtype(x_dtype) || !known_dtype(y_dtype)) return fail(SLSTM_EINVAL, "unknown dtype %d, %d", (int)x_dtype, (int)y_dtype);
+  if (!(eps >= 0.0f) || std::isinf(eps)) return fail(SLSTM_EINVAL, "eps must be finite and >= 0");
+  if (rows == 0) return SLSTM_OK;
+  if (x == nullptr || y == nullptr) return fail(SLSTM_EINVAL, "x and y must not be NULL");
+  if (!aligned(x, elem_size(x_dtype)) || !aligned(y, elem_size(y_dtype)) || !aligned(weight, 4) || !aligned(bias, 4) ||
+      !aligned(mean, 4) || !aligned(rstd, 4))
+    return fail(SLSTM_EINVAL, "x, y, weight, bias, mean or rstd misaligned");
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  HIP_TRY(timed(SLSTM_KERNEL_LAYER_NORM, st, [&] {
+    return slstm::launch_norm_forward(x, x_dtype == SLSTM_BF16, weight, bias, eps, y, y_dtype == SLSTM_BF16, mean, rstd,
+                                      rows, width, st);
+  }));
+  return SLSTM_OK;
+}
+
+size_t slstm_layer_norm_backward_workspace_bytes(int64_t rows, int width) {
+  if (check_norm(rows, width) != SLSTM_OK) return 0;
+  return align_up(static_cast<size_t>(rows > 0 ? slstm::norm_backward_rows(rows, width) : 1) * 2 * width * sizeof(float));
+}
+
+slstm_status slstm_layer_norm_backward(const void* x, slstm_dtype x_dtype, const void* g_y, slstm_dtype g_dtype,
+                                       const float* mean, const float* rstd, const float* weight, void* dx,
+                                       float* dweight, float* dbias, int64_t rows, int width, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  g_err[0] = '\0';
+  slstm_status s = check_norm(rows, width);
+  if (s != SLSTM_OK) return s;
+  if (!known_dtype(x_dtype) || !known_dtype(g_dtype)) return fail(SLSTM_EINVAL, "unknown dtype %d, %d", (int)x_dtype, (int)g_dtype);
+  if (rows > 0 && (x == nullptr || g_y == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr))
+    return fail(SLSTM_EINVAL, "x, g_y, mean, rstd and dx must not be NULL");
+  if (!aligned(x, elem_size(x_dtype)) || !aligned(dx, elem_size(x_dtype)) || !aligned(g_y, elem_size(g_dtype)) ||
+      !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(weight, 4) || !aligned(dweight, 4) || !aligned(dbias, 4))
+    return fail(SLSTM_EINVAL, "x, g_y, dx, mean, rstd, weight, dweight or dbias misaligned");
+  if (dweight != nullptr || dbias != nullptr) {
+    s = check_workspace(workspace, workspace_bytes, slstm_layer_norm_backward_workspace_bytes(rows, width));
+    if (s != SLSTM_OK) return s;
+  }
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  HIP_TRY(timed(SLSTM_KERNEL_LAYER_NORM, st, [&] {
+    return slstm::launch_norm_backward(x, x_dtype == SLSTM_BF16, g_y, g_dtype == SLSTM_BF16, mean, rstd, weight, dx,
+                                       dweight, dbias, static_cast<float*>(workspace), rows, width, st);
+  }));
+  return SLSTM_OK;
+}
+
+size_t slstm_linear_attention_workspace_bytes(int B, int T, int n_heads, int d_key, int d_value, int n_seqs) {
+  if (check_linear(B, T, n_heads, d_key, d_value, n_seqs) != SLSTM_OK) return 0;
+  return linear_plan(B, T, n_heads, d_key, d_value, n_seqs, 1).total;
+}
+
+slstm_status slstm_linear_attention_forward(const slstm_heads* q, const slstm_heads* k, const slstm_heads* v,
+                                            slstm_dtype dtype, const float* log_decay, int decay_per_head,
+                                            const float* state0, float scale, const slstm_heads* out,
+                                            float* final_state, int B, int T, int n_heads, int d_key, int d_value,
+                                            const int* cu_seqlens, int n_seqs, void* workspace,
+                                            size_t workspace_bytes, void* stream) {
+  g_err[0] = '\0';
+  slstm_status s = check_linear_common(q, k, v, dtype, log_decay, state0, scale, B, T, n_heads, d_key, d_value, cu_seqlens, n_seqs);
+  if (s != SLSTM_OK) return s;
+  s = check_heads_view(out, "out", dtype, T == 0);
+  if (s != SLSTM_OK) return s;
+  if (!aligned(final_state, 16)) return fail(SLSTM_EINVAL, "final_state must be 16-byte aligned");
+  const LinPlan p = linear_plan(B, T, n_heads, d_key, d_value, n_seqs, 1);
+  s = check_workspace(workspace, workspace_bytes, p.total);
+  if (s != SLSTM_OK) return s;
+  slstm::LinLaunch a;
+  linear_base(a, log_decay, decay_per_head, B, T, n_heads, cu_seqlens, n_seqs);
+  slstm::LinRole& r = a.role[0];
+  r.q = view_of(q), r.k = view_of(k), r.v = view_of(v), r.out = view_of(out);
+  r.KD = d_key, r.VD = d_value, r.o_scale = scale;
+  r.state_in = state0, r.state_out = final_state;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  HIP_TRY(timed(SLSTM_KERNEL_LINEAR_ATTENTION, st, [&] {
+    return linear_run(a, p, dtype == SLSTM_BF16, slstm::LinPass::kForward, workspace, st);
+  }));
+  return SLSTM_OK;
+}
+
+slstm_status slstm_linear_attention_step(const slstm_heads* q, const slstm_heads* k, const slstm_heads* v,
+                                         slstm_dtype dtype, const float* log_decay, int decay_per_head, float* state,
+                                         const int* slots, int n_slots, float scale, void* out, int B, int n_heads,
+                                         int d_key, int d_value, void* stream) {
+  g_err[0] = '\0';
+  slstm_status s = check_linear_common(q, k, v, dtype, log_decay, state, scale, B, 1, n_heads, d_key, d_value, nullptr, 0);
+  if (s != SLSTM_OK) return s;
+  if (state == nullptr || out == nullptr) return fail(SLSTM_EINVAL, "state and out must not be NULL");
+  if (!aligned(out, 16) || !aligned(slots, 4)) return fail(SLSTM_EINVAL, "out must be 16-byte and slots 4-byte aligned");
+  if (n_slots < 1 || (slots == nullptr && n_slots < B))
+    return fail(SLSTM_EINVAL, "n_slots must be >= 1, and >= B without slots (got %d, B = %d)", n_slots, B);
+  slstm::LinStep a;
+  a.q = view_of(q), a.k = view_of(k), a.v = view_of(v);
+  a.out = out, a.gate = log_decay, a.gate_b = decay_per_head ? 0 : n_heads, a.gate_h = 1;
+  a.state = state, a.slots = slots, a.n_slots = n_slots, a.B = B, a.H = n_heads, a.KD = d_key, a.VD = d_value;
+  a.scale = scale;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  HIP_TRY(timed(SLSTM_KERNEL_LINEAR_STEP, st, [&] { return slstm::launch_linear_step(dtype == SLSTM_BF16, a, st); }));
+  return SLSTM_OK;
+}
+
+size_t slstm_linear_attention_backward_workspace_bytes(int B, int T, int n_heads, int d_key, int d_value, int n_seqs) {
+  if (check_linear(B, T, n_heads, d_key, d_value, n_seqs) != SLSTM_OK) return 0;
+  return std::max(kAlign, linear_plan(B, T, n_heads, d_key, d_value, n_seqs, 3).total);
+}
+
+slstm_status slstm_linear_attention_backward(const slstm_heads* q, const slstm_heads* k, const slstm_heads* v,
+                                             slstm_dtype dtype, const float* log_decay, int decay_per_head,
+                                             const float* state0, float scale, const slstm_heads* g_out,
+                                             const float* g_final, const slstm_heads* dq, const slstm_heads* dk,
+                                             const slstm_heads* dv, float* dlog_decay, float* dstate0, int B, int T,
+                                             int n_heads, int d_key, int d_value, const int* cu_seqlens, int n_seqs,
+                                             void* workspace, size_t workspace_bytes, void* stream) {
+  g_err[0] = '\0';
+  slstm_status s = check_linear_common(q, k, v, dtype, log_decay, state0, scale, B, T, n_heads, d_key, d_value, cu_seqlens, n_seqs);
+  if (s != SLSTM_OK) return s;
+  for (auto& x : {std::make_pair(g_out, "g_out"), std::make_pair(dq, "dq"), std::make_pair(dk, "dk"), std::make_pair(dv, "dv")}) {
+    s = check_heads_view(x.first, x.second, dtype, T == 0);
+    if (s != SLSTM_OK) return s;
+  }
+  if (!aligned(g_final, 16) || !aligned(dstate0, 16) || !aligned(dlog_decay, 4))
+    return fail(SLSTM_EINVAL, "g_final and dstate0 must be 16-byte and dlog_decay 4-byte aligned");
+  if (dlog_decay != nullptr && decay_per_head)
+    return fail(SLSTM_EINVAL, "a decay fixed per head has no gradient: pass log_decay as (B, T, n_heads)");
+  const LinPlan p = linear_plan(B, T, n_heads, d_key, d_value, n_seqs, 3);
+  s = check_workspace(workspace, workspace_bytes, std::max(kAlign, p.total));
+  if (s != SLSTM_OK) return s;
+  slstm::LinLaunch a;
+  linear_base(a, log_decay, decay_per_head, B, T, n_heads, cu_seqlens, n_seqs);
+  a.n_roles = 3;
+  // dq = LA(g, v, k) on S^T; dk = LA(v, g, q) backward in time on L^T; dv = LA(k, q, g) on L
+  slstm::LinRole &rq = a.role[0], &rk = a.role[1], &rv = a.role[2];
+  rq.q = view_of(g_out), rq.k = view_of(v), rq.v = view_of(k), rq.out = view_of(dq);
+  rq.KD = d_value, rq.VD = d_key, rq.o_scale = scale, rq.state_in = state0, rq.transposed = 1;
+  rk.q = view_of(v), rk.k = view_of(g_out), rk.v = view_of(q), rk.out = view_of(dk);
+  rk.KD = d_value, rk.VD = d_key, rk.v_scale = scale, rk.reverse = 1, rk.state_in = g_final, rk.transposed = 1;
+  rv.q = view_of(k), rv.k = view_of(q), rv.v = view_of(g_out), rv.out = view_of(dv);
+  rv.KD = d_key, rv.VD = d_value, rv.v_scale = scale, rv.reverse = 1, rv.state_in = g_final, rv.state_out = dstate0;
+  float *r = nullptr, *c = nullptr, *edge = nullptr;
+  if (dlog_decay != nullptr) {
+    r = at<float>(workspace, p.r), c = at<float>(workspace, p.c);
+    rq.dot = view_of(q), rq.dot_out = r;
+    rk.dot = view_of(k), rk.dot_out = c;
+    if (g_final != nullptr) {
+      edge = at<float>(workspace, p.edge);
+      rq.edge = g_final, rq.edge_out = edge;
+    }
+  }
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const bool bf16 = dtype == SLSTM_BF16;
+  HIP_TRY(timed(SLSTM_KERNEL_LINEAR_ATTENTION, st, [&]() -> hipError_t {
+    HIP_RET(linear_run(a, p, bf16, dlog_decay != nullptr ? slstm::LinPass::kExact : slstm::LinPass::kForward, workspace, st));
+    if (dlog_decay == nullptr || T == 0) return hipSuccess;
+    return slstm::launch_linear_gate_gradient(r, c, edge, a, dlog_decay, st);
+  }));
+  return SLSTM_OK;
 }
 
 slstm_status slstm_profile_enable(int on) {

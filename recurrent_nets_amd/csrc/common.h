@@ -22,6 +22,16 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
   return static_cast<uint16_t>((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
 }
 
+// two float32 values as a pair of bfloat16 (the first in the low half), rounded to nearest, ties
+// to even, by the conversion instruction; NaN stays NaN
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  union { bf16x2_t b; uint32_t u; } r;
+  r.b = __builtin_convertvector(f32x2_t{lo, hi}, bf16x2_t);
+  return r.u;
+}
+
 // Load one gate pre-activation, stored as float32 or bfloat16.
 template <bool BF16>
 __device__ __forceinline__ float load_p(const void* __restrict__ P, i64 idx) {
@@ -184,6 +194,19 @@ __device__ __forceinline__ float quad_perm(float v) {
 // ---- wave / block maximum --------------------------------------------------------------------
 __device__ __forceinline__ float wave_max(float v) {
   for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
+  return v;
+}
+
+// Sum over the 64 lanes, the same bits in every lane: lane exchanges within rows of 16 (DPP), then
+// across the rows and halves of the wave. Every addition is of the same two values in both lanes
+// of an exchange, and float addition commutes.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += quad_perm<1, 0, 3, 2>(v);
+  v += quad_perm<2, 3, 0, 1>(v);
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xf, 0xf, false));  // row_half_mirror
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xf, 0xf, false));  // row_mirror
+  v += __shfl_xor(v, 16, kWave);
+  v += __shfl_xor(v, 32, kWave);
   return v;
 }
 

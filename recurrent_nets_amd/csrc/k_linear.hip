@@ -1,0 +1,255 @@
+// Linear attention with a decay for each head: the single step, the join of the time axis's
+// segments, the gradient of the log decays, and the choice of the walk's kernel (linear.h).
+#include "common.h"
+#include "kernels.h"
+
+namespace slstm {
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kZeroDecay = -104.0f;  // e^-104 is below float32's smallest subnormal
+
+__device__ __forceinline__ float decay_of(float g) {
+  return g <= kZeroDecay ? 0.0f : __builtin_amdgcn_exp2f(g * 1.44269504088896340736f);
+}
+
+// ---- one step ------------------------------------------------------------------------------------
+// S <- e^g S + k v^T, o = scale S^T q, per (batch row, head). Bound by the state's bytes, read and
+// written once. A workgroup of 256 takes 32 columns: 8 lanes of 4 columns (a 128-byte line of each
+// state row) by 32 rows, each lane's NR rows in registers, loaded before any is used. The rows'
+// parts of o are added over the wave by lane exchanges and over the 4 waves in LDS, in order.
+constexpr int kStepCols = 32;
+
+template <bool BF16>
+__device__ __forceinline__ float step_load(const void* base, i64 at) {
+  return load_p<BF16>(base, at);
+}
+
+template <bool BF16, int NR>
+__global__ __launch_bounds__(256) void linear_step_kernel(const LinStep a) {
+  __shared__ float part[4][kStepCols];
+  const int tiles = (a.VD + kStepCols - 1) / kStepCols;
+  const int tile = blockIdx.x % tiles;
+  const int bh = blockIdx.x / tiles;
+  const int b = bh / a.H, h = bh - b * a.H;
+  const int cx = threadIdx.x & 7, ry = threadIdx.x >> 3;
+  const int col = tile * kStepCols + 4 * cx;
+  const bool in = col < a.VD;
+  const int slot = a.slots != nullptr ? a.slots[b] : b;
+  const i64 at_o = (static_cast<i64>(b) * a.H + h) * a.VD + col;
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (slot >= 0 && slot < a.n_slots && in) {
+    float* S = a.state + (static_cast<i64>(slot) * a.H + h) * a.KD * a.VD + col;
+    f32x4 s[NR];
+    float q[NR], k[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int row = i * 32 + ry;
+      s[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, q[i] = 0.0f, k[i] = 0.0f;
+      if (row < a.KD) {
+        s[i] = *reinterpret_cast<const f32x4*>(S + static_cast<i64>(row) * a.VD);
+        q[i] = step_load<BF16>(a.q.data, b * a.q.sb + h * a.q.sh + row);
+        k[i] = step_load<BF16>(a.k.data, b * a.k.sb + h * a.k.sh + row);
+      }
+    }
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = step_load<BF16>(a.v.data, b * a.v.sb + h * a.v.sh + col + e);
+    const float d = decay_of(a.gate[b * a.gate_b + h * a.gate_h]);
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int row = i * 32 + ry;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[i][e] = fmaf(s[i][e], d, k[i] * v[e]);
+        o[e] = fmaf(s[i][e], q[i], o[e]);
+      }
+      if (row < a.KD) *reinterpret_cast<f32x4*>(S + static_cast<i64>(row) * a.VD) = s[i];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    o[e] += __shfl_xor(o[e], 8, kWave);
+    o[e] += __shfl_xor(o[e], 16, kWave);
+    o[e] += __shfl_xor(o[e], 32, kWave);
+  }
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) < 8) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[wave][4 * cx + e] = o[e];
+  }
+  __syncthreads();
+  if (threadIdx.x < 8 && in) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      o[e] = part[0][4 * cx + e];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) o[e] += part[w][4 * cx + e];
+      o[e] *= a.scale;
+    }
+    if constexpr (BF16) {
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at_o) = u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+    } else {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at_o) = o;
+    }
+  }
+}
+
+// ---- the segments' states, joined ------------------------------------------------------------------
+// X <- state entering the sequence; for each segment but the last, X <- decay X + (its own state),
+// left in place of that state: what the next segment starts from.
+__global__ __launch_bounds__(256) void linear_join_kernel(const LinLaunch a) {
+  const LinRole& R = a.role[blockIdx.z];
+  const int n = R.KD * R.VD;
+  const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
+  if (e >= n) return;
+  const int seq = blockIdx.x / a.H, head = blockIdx.x % a.H;
+  int slot = seq * a.n_seg, segs = a.n_seg;
+  if (a.cu != nullptr) {
+    const int start = min(max(a.cu[seq], 0), a.T);
+    const int len = max(0, min(max(a.cu[seq + 1], 0), a.T) - start);
+    slot = start / a.seg_len + seq;
+    segs = (len + a.seg_len - 1) / a.seg_len;
+  }
+  f32x4 X = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (segs > 1 && R.state_in != nullptr) {
+    const float* from = R.state_in + static_cast<i64>(blockIdx.x) * n;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = (e + i) / R.VD, v = (e + i) - k * R.VD;
+      X[i] = R.transposed ? from[v * R.KD + k] : from[e + i];
+    }
+  }
+  for (int g = 0; g + 1 < segs; ++g) {
+    const i64 at = static_cast<i64>(slot + g) * a.H + head;
+    f32x4* own = reinterpret_cast<f32x4*>(R.seg_states + at * n + e);
+    const float d = R.seg_decays[at];
+    const f32x4 s = *own;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) X[i] = fmaf(X[i], d, s[i]);
+    *own = X;
+  }
+}
+
+// ---- the gradient of the log decays ------------------------------------------------------------------
+// dL/dg_t = <L_t, e^{g_t} S_{t-1}>, for which dg_t - dg_{t+1} = q_t . dq_t - k_t . dk_t: a sum from
+// the end, begun with <gradient of the final state, final state>. One workgroup a (sequence, head),
+// 1024 steps at a time from the end. The sums run in 64 bits: their terms cancel over the whole
+// sequence while dg stays of the size that the decays remember. Bytes are those of three floats a
+// step, a few per cent of the operands'.
+__global__ __launch_bounds__(256) void linear_gate_gradient_kernel(const float* __restrict__ r, const float* __restrict__ c,
+                                                                   const float* __restrict__ edge, const LinLaunch a,
+                                                                   float* __restrict__ dgate) {
+  __shared__ double waves[4];
+  const int seq = blockIdx.x / a.H, head = blockIdx.x % a.H;
+  int start = 0, len = a.T;
+  i64 row = seq;
+  if (a.cu != nullptr) {
+    start = min(max(a.cu[seq], 0), a.T);
+    len = max(0, min(max(a.cu[seq + 1], 0), a.T) - start);
+    row = 0;
+  }
+  const i64 base = (row * a.H + head) * static_cast<i64>(a.T) + start;
+  const float* gate = a.gate + row * a.gate_b + start * a.gate_t + head * a.gate_h;
+  float* out = dgate + (row * static_cast<i64>(a.T) + start) * a.H + head;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  double carry = edge != nullptr ? static_cast<double>(edge[blockIdx.x]) : 0.0;
+  for (int end = len; end > 0; end -= 1024) {
+    // thread i holds steps end - 1 - 4 i .. end - 4 - 4 i, latest first
+    double s[4], total = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = end - 1 - 4 * static_cast<int>(threadIdx.x) - i;
+      if (t >= 0) total += static_cast<double>(r[base + t]) - static_cast<double>(c[base + t]);
+      s[i] = total;
+    }
+    double inc = total;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double up = __shfl_up(inc, off, 64);
+      if (lane >= off) inc += up;
+    }
+    if (lane == 63) waves[wave] = inc;
+    __syncthreads();
+    double before = carry + (inc - total);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) before += waves[w];
+      carry += waves[w];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = end - 1 - 4 * static_cast<int>(threadIdx.x) - i;
+      // a decay of zero, or one of a zero state, has no gradient
+      const bool none = t >= 0 && (gate[t * a.gate_t] <= kZeroDecay || (t == 0 && a.role[0].state_in == nullptr));
+      if (t >= 0) out[static_cast<i64>(t) * a.H] = none ? 0.0f : static_cast<float>(before + s[i]);
+    }
+  }
+}
+
+template <bool BF16>
+hipError_t step_as(const LinStep& a, hipStream_t st) {
+  const long long blocks = static_cast<long long>(a.B) * a.H * ((a.VD + kStepCols - 1) / kStepCols);
+  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+  const unsigned g = static_cast<unsigned>(blocks);
+  if (a.KD <= 32) linear_step_kernel<BF16, 1><<<g, 256, 0, st>>>(a);
+  else if (a.KD <= 64) linear_step_kernel<BF16, 2><<<g, 256, 0, st>>>(a);
+  else if (a.KD <= 128) linear_step_kernel<BF16, 4><<<g, 256, 0, st>>>(a);
+  else linear_step_kernel<BF16, 8><<<g, 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int linear_blocks(int width) {
+  int b = 1;
+  while (b * 32 < width) b *= 2;
+  return b;
+}
+
+hipError_t launch_linear_step(bool bf16, const LinStep& a, hipStream_t st) {
+  return bf16 ? step_as<true>(a, st) : step_as<false>(a, st);
+}
+
+// Roles of equal padded widths share a launch; the others follow in launches of their own.
+hipError_t launch_linear_walk(bool bf16, const LinLaunch& a, LinPass pass, hipStream_t st) {
+  bool done[kLinMaxRoles] = {};
+  for (int i = 0; i < a.n_roles; ++i) {
+    if (done[i]) continue;
+    const int kb = linear_blocks(a.role[i].KD), vb = linear_blocks(a.role[i].VD);
+    LinLaunch part = a;
+    part.n_roles = 0;
+    for (int j = i; j < a.n_roles; ++j)
+      if (linear_blocks(a.role[j].KD) == kb && linear_blocks(a.role[j].VD) == vb) {
+        part.role[part.n_roles++] = a.role[j];
+        done[j] = true;
+      }
+    hipError_t e;
+    switch (kb) {
+      case 1: e = launch_linear_keys32(bf16, vb, part, pass, st); break;
+      case 2: e = launch_linear_keys64(bf16, vb, part, pass, st); break;
+      case 4: e = launch_linear_keys128(bf16, vb, part, pass, st); break;
+      default: e = launch_linear_keys256(bf16, vb, part, pass, st); break;
+    }
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_linear_join(const LinLaunch& a, hipStream_t st) {
+  const int n = a.role[0].KD * a.role[0].VD;  // the roles' states have one size
+  linear_join_kernel<<<dim3(static_cast<unsigned>(a.n_seqs) * a.H, (n / 4 + 255) / 256, a.n_roles), 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_gate_gradient(const float* r, const float* c, const float* edge, const LinLaunch& a,
+                                       float* dgate, hipStream_t st) {
+  linear_gate_gradient_kernel<<<static_cast<unsigned>(a.n_seqs) * a.H, 256, 0, st>>>(r, c, edge, a, dgate);
+  return hipGetLastError();
+}
+
+}  // namespace slstm

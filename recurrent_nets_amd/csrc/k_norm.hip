@@ -1,0 +1,549 @@
+// Layer norm over the last axis of a (rows, width) tensor, forward and backward.
+//
+//   mean = sum x / D;  var = sum (x - mean)^2 / D;  rstd = 1 / sqrt(var + eps)
+//   xh = (x - mean) rstd;  y = xh w + b                       (w, b optional: 1 and 0)
+// and, for the gradient g of y,
+//   gw = g w;  dx = rstd (gw - mean(gw) - xh mean(gw xh))
+//   dw = sum over rows of g xh;  db = sum over rows of g
+//
+// HBM bound: the forward reads x and writes y once, the backward reads x and g and writes dx
+// once. A row stays in registers between its reductions: kNormLane values a lane, one wave for
+// up to 64 kNormLane columns and 2, 4, 8 or 16 waves (reductions through LDS) beyond; rows wider
+// than 16 waves hold are read again for each pass over them (the cache serves what it can).
+// Sums are float32: the lane's own values, then the wave by lane exchanges, then the waves in
+// order, so results are the same on every run. The variance is that of the centred values.
+//
+// Workgroups walk the rows with a fixed stride, the weights in registers; the next row's loads
+// are issued before the present row's reductions. The backward keeps each lane's columns of dw
+// and db in registers over all rows of the walk, adds the workgroup's waves in LDS and writes one
+// partial row per workgroup; a second kernel adds the partial rows in a fixed order (no atomics).
+#include "common.h"
+#include "kernels.h"
+
+namespace slstm {
+
+namespace {
+
+constexpr int kNormThreads = 256;    // workgroup of the forms with up to 4 waves a row
+constexpr int kNormLane = 16;        // columns a lane holds
+constexpr int kNormMaxWaves = 16;    // waves a row in registers may take
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// VEC consecutive values as float32
+template <bool BF16, int VEC>
+__device__ __forceinline__ void load_vec(const void* base, i64 at, float (&v)[VEC]) {
+  if constexpr (BF16) {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+    if constexpr (VEC == 1) {
+      v[0] = bf16_to_f32(*p);
+    } else {
+      uint32_t w[VEC / 2];
+      if constexpr (VEC == 8) {
+        const u32x4 t = *reinterpret_cast<const u32x4*>(p);
+        w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
+      } else {
+        const u32x2 t = *reinterpret_cast<const u32x2*>(p);
+        w[0] = t.x, w[1] = t.y;
+      }
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  } else {
+    const float* p = static_cast<const float*>(base) + at;
+    if constexpr (VEC == 1) {
+      v[0] = *p;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 4; ++i) {
+        const f32x4 t = reinterpret_cast<const f32x4*>(p)[i];
+        v[4 * i] = t.x, v[4 * i + 1] = t.y, v[4 * i + 2] = t.z, v[4 * i + 3] = t.w;
+      }
+    }
+  }
+}
+
+template <bool BF16, int VEC>
+__device__ __forceinline__ void store_vec(void* base, i64 at, const float (&v)[VEC]) {
+  if constexpr (BF16) {
+    uint16_t* p = static_cast<uint16_t*>(base) + at;
+    if constexpr (VEC == 1) {
+      *p = f32_to_bf16_rne(v[0]);
+    } else {
+      uint32_t w[VEC / 2];
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+      if constexpr (VEC == 8) {
+        *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+      } else {
+        *reinterpret_cast<u32x2*>(p) = u32x2{w[0], w[1]};
+      }
+    }
+  } else {
+    float* p = static_cast<float*>(base) + at;
+    if constexpr (VEC == 1) {
+      *p = v[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 4; ++i)
+        reinterpret_cast<f32x4*>(p)[i] = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+    }
+  }
+}
+
+// N sums over the W waves of a row's group, each lane holding its part; every lane of the group
+// gets the totals. `red` is this group's LDS, W * N floats; the waves' sums are added in order.
+template <int W, int N>
+__device__ __forceinline__ void group_sum(float (&s)[N], float* red, int wave_in_group) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] = wave_sum(s[i]);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) red[wave_in_group * N + i] = s[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float t = red[i];
+#pragma unroll
+      for (int w = 1; w < W; ++w) t += red[w * N + i];
+      s[i] = t;
+    }
+    __syncthreads();
+  }
+}
+
+// ---- forward ------------------------------------------------------------------------------------
+// W waves a row, NCH chunks of VEC columns a lane: chunk c of the group's lane gl holds columns
+// (c * 64 W + gl) * VEC and the VEC - 1 after it.
+template <bool XB, bool YB, int VEC, int NCH, int W>
+__global__ __launch_bounds__(W > 4 ? W * 64 : kNormThreads) void norm_forward_kernel(
+    const void* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias, float eps,
+    void* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, i64 rows, int D) {
+  constexpr int kThreads = W > 4 ? W * 64 : kNormThreads;
+  constexpr int kGroups = kThreads / (64 * W);
+  __shared__ float red[kGroups * W];
+  const int group = threadIdx.x / (64 * W);
+  const int gl = threadIdx.x % (64 * W);
+  float* my_red = red + group * W;
+  const float inv = 1.0f / static_cast<float>(D);
+  float w[NCH][VEC], b[NCH][VEC];
+  int col[NCH];
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    col[c] = (c * 64 * W + gl) * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) w[c][e] = 1.0f, b[c][e] = 0.0f;
+    if (col[c] < D) {
+      if (weight != nullptr) load_vec<false, VEC>(weight, col[c], w[c]);
+      if (bias != nullptr) load_vec<false, VEC>(bias, col[c], b[c]);
+    }
+  }
+  float nx[NCH][VEC];
+  auto fetch = [&](i64 r) {
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) nx[c][e] = 0.0f;
+      if (r < rows && col[c] < D) load_vec<XB, VEC>(x, r * D + col[c], nx[c]);
+    }
+  };
+  const i64 stride = static_cast<i64>(gridDim.x) * kGroups;
+  // every group of a workgroup walks the same number of rows: the barriers match
+  i64 r = static_cast<i64>(blockIdx.x) * kGroups + group;
+  fetch(r);
+  for (i64 r0 = static_cast<i64>(blockIdx.x) * kGroups; r0 < rows; r0 += stride, r += stride) {
+    float v[NCH][VEC];
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        v[c][e] = nx[c][e];
+        s[0] += v[c][e];
+      }
+    fetch(r + stride);
+    group_sum<W>(s, my_red, gl >> 6);
+    const float mean = s[0] * inv;
+    s[0] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+      if (col[c] < D) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          v[c][e] -= mean;
+          s[0] = fmaf(v[c][e], v[c][e], s[0]);
+        }
+      }
+    group_sum<W>(s, my_red, gl >> 6);
+    const float rstd = 1.0f / sqrtf(fmaf(s[0], inv, eps));
+    if (r >= rows) continue;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+      if (col[c] < D) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[c][e] = fmaf(v[c][e] * rstd, w[c][e], b[c][e]);
+        store_vec<YB, VEC>(y, r * D + col[c], v[c]);
+      }
+    if (gl == 0) {
+      if (mean_out != nullptr) mean_out[r] = mean;
+      if (rstd_out != nullptr) rstd_out[r] = rstd;
+    }
+  }
+}
+
+// rows wider than 16 waves hold: one workgroup a row, three passes over it
+template <bool XB, bool YB>
+__global__ __launch_bounds__(1024) void norm_forward_wide_kernel(
+    const void* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias, float eps,
+    void* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, i64 rows, int D) {
+  __shared__ float red[16];
+  const float inv = 1.0f / static_cast<float>(D);
+  for (i64 r = blockIdx.x; r < rows; r += gridDim.x) {
+    float s[1] = {0.0f};
+    float v[1];
+    for (int c = threadIdx.x; c < D; c += 1024) {
+      load_vec<XB, 1>(x, r * D + c, v);
+      s[0] += v[0];
+    }
+    group_sum<16>(s, red, threadIdx.x >> 6);
+    const float mean = s[0] * inv;
+    s[0] = 0.0f;
+    for (int c = threadIdx.x; c < D; c += 1024) {
+      load_vec<XB, 1>(x, r * D + c, v);
+      s[0] = fmaf(v[0] - mean, v[0] - mean, s[0]);
+    }
+    group_sum<16>(s, red, threadIdx.x >> 6);
+    const float rstd = 1.0f / sqrtf(fmaf(s[0], inv, eps));
+    for (int c = threadIdx.x; c < D; c += 1024) {
+      load_vec<XB, 1>(x, r * D + c, v);
+      v[0] = fmaf((v[0] - mean) * rstd, weight != nullptr ? weight[c] : 1.0f, bias != nullptr ? bias[c] : 0.0f);
+      store_vec<YB, 1>(y, r * D + c, v);
+    }
+    if (threadIdx.x == 0) {
+      if (mean_out != nullptr) mean_out[r] = mean;
+      if (rstd_out != nullptr) rstd_out[r] = rstd;
+    }
+  }
+}
+
+// ---- backward -----------------------------------------------------------------------------------
+// part: gridDim.x rows of 2 D floats (dw, then db), written when want_w
+template <bool XB, bool GB, int VEC, int NCH, int W>
+__global__ __launch_bounds__(W > 4 ? W * 64 : kNormThreads) void norm_backward_kernel(
+    const void* __restrict__ x, const void* __restrict__ g, const float* __restrict__ mean,
+    const float* __restrict__ rstd, const float* __restrict__ weight, void* __restrict__ dx,
+    float* __restrict__ part, i64 rows, int D) {
+  constexpr int kThreads = W > 4 ? W * 64 : kNormThreads;
+  constexpr int kGroups = kThreads / (64 * W);
+  __shared__ float red[kGroups * W * 2];
+  // the groups' sums of dw and db meet here, one chunk of columns at a time
+  __shared__ float meet[kGroups > 1 ? 2 * kThreads * VEC : 1];
+  const int group = threadIdx.x / (64 * W);
+  const int gl = threadIdx.x % (64 * W);
+  float* my_red = red + group * W * 2;
+  const float inv = 1.0f / static_cast<float>(D);
+  float w[NCH][VEC], dw[NCH][VEC], db[NCH][VEC];
+  int col[NCH];
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    col[c] = (c * 64 * W + gl) * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) w[c][e] = 1.0f, dw[c][e] = 0.0f, db[c][e] = 0.0f;
+    if (col[c] < D && weight != nullptr) load_vec<false, VEC>(weight, col[c], w[c]);
+  }
+  const i64 stride = static_cast<i64>(gridDim.x) * kGroups;
+  i64 r = static_cast<i64>(blockIdx.x) * kGroups + group;
+  constexpr bool kAhead = W < 16;  // 1024 threads leave 128 registers: no room for a second row
+  float nx[NCH][VEC], ng[NCH][VEC], nm, nr;
+  auto fetch = [&](i64 rr) {
+    const bool in = rr < rows;
+    nm = in ? mean[rr] : 0.0f;
+    nr = in ? rstd[rr] : 0.0f;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) nx[c][e] = 0.0f, ng[c][e] = 0.0f;
+      if (in && col[c] < D) {
+        load_vec<XB, VEC>(x, rr * D + col[c], nx[c]);
+        load_vec<GB, VEC>(g, rr * D + col[c], ng[c]);
+      }
+    }
+  };
+  if constexpr (kAhead) fetch(r);
+  for (i64 r0 = static_cast<i64>(blockIdx.x) * kGroups; r0 < rows; r0 += stride, r += stride) {
+    float xh[NCH][VEC], gw[NCH][VEC];
+    if constexpr (!kAhead) fetch(r);
+    const float m = nm, rs = nr;
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+      if (col[c] < D) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float gv = ng[c][e];
+          xh[c][e] = (nx[c][e] - m) * rs;
+          dw[c][e] = fmaf(gv, xh[c][e], dw[c][e]);
+          db[c][e] += gv;
+          gw[c][e] = gv * w[c][e];
+          s[0] += gw[c][e];
+          s[1] = fmaf(gw[c][e], xh[c][e], s[1]);
+        }
+      }
+    if constexpr (kAhead) fetch(r + stride);
+    group_sum<W>(s, my_red, gl >> 6);
+    if (r >= rows) continue;
+    const float a = s[0] * inv, bb = s[1] * inv;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+      if (col[c] < D) {
+        float o[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = rs * (gw[c][e] - fmaf(xh[c][e], bb, a));
+        store_vec<XB, VEC>(dx, r * D + col[c], o);
+      }
+  }
+  if (part == nullptr) return;
+  float* out = part + static_cast<i64>(blockIdx.x) * 2 * D;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    if constexpr (kGroups > 1) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        meet[threadIdx.x * VEC + e] = dw[c][e];
+        meet[(kThreads + threadIdx.x) * VEC + e] = db[c][e];
+      }
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int k = 1; k < kGroups; ++k)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            dw[c][e] += meet[(k * 64 * W + gl) * VEC + e];
+            db[c][e] += meet[(kThreads + k * 64 * W + gl) * VEC + e];
+          }
+      }
+      __syncthreads();
+    }
+    if (group == 0 && col[c] < D) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        out[col[c] + e] = dw[c][e];
+        out[D + col[c] + e] = db[c][e];
+      }
+    }
+  }
+}
+
+// rows wider than 16 waves hold: one workgroup a row; dw and db by columns in a kernel of its own
+template <bool XB, bool GB>
+__global__ __launch_bounds__(1024) void norm_backward_wide_kernel(
+    const void* __restrict__ x, const void* __restrict__ g, const float* __restrict__ mean,
+    const float* __restrict__ rstd, const float* __restrict__ weight, void* __restrict__ dx, i64 rows, int D) {
+  __shared__ float red[32];
+  const float inv = 1.0f / static_cast<float>(D);
+  for (i64 r = blockIdx.x; r < rows; r += gridDim.x) {
+    const float m = mean[r], rs = rstd[r];
+    float s[2] = {0.0f, 0.0f};
+    float xv[1], gv[1];
+    for (int c = threadIdx.x; c < D; c += 1024) {
+      load_vec<XB, 1>(x, r * D + c, xv);
+      load_vec<GB, 1>(g, r * D + c, gv);
+      const float gw = gv[0] * (weight != nullptr ? weight[c] : 1.0f);
+      s[0] += gw;
+      s[1] = fmaf(gw, (xv[0] - m) * rs, s[1]);
+    }
+    group_sum<16>(s, red, threadIdx.x >> 6);
+    const float a = s[0] * inv, b = s[1] * inv;
+    for (int c = threadIdx.x; c < D; c += 1024) {
+      load_vec<XB, 1>(x, r * D + c, xv);
+      load_vec<GB, 1>(g, r * D + c, gv);
+      const float gw = gv[0] * (weight != nullptr ? weight[c] : 1.0f);
+      const float o[1] = {rs * (gw - fmaf((xv[0] - m) * rs, b, a))};
+      store_vec<XB, 1>(dx, r * D + c, o);
+    }
+  }
+}
+
+// the columns' sums of wide rows: block (column block, row block) writes one row of partial sums
+template <bool XB, bool GB>
+__global__ __launch_bounds__(256) void norm_columns_kernel(const void* __restrict__ x, const void* __restrict__ g,
+                                                           const float* __restrict__ mean,
+                                                           const float* __restrict__ rstd, float* __restrict__ part,
+                                                           i64 rows, int D) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= D) return;
+  float dw = 0.0f, db = 0.0f;
+  for (i64 r = blockIdx.y; r < rows; r += gridDim.y) {
+    float xv[1], gv[1];
+    load_vec<XB, 1>(x, r * D + c, xv);
+    load_vec<GB, 1>(g, r * D + c, gv);
+    dw = fmaf(gv[0], (xv[0] - mean[r]) * rstd[r], dw);
+    db += gv[0];
+  }
+  float* out = part + static_cast<i64>(blockIdx.y) * 2 * D;
+  out[c] = dw;
+  out[D + c] = db;
+}
+
+// dw[c] and db[c]: the n partial rows in a fixed order; wave k of a workgroup takes rows k, k + 16,
+// ..., a lane one column of the 2 D
+__global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restrict__ part, int n, int D,
+                                                           float* __restrict__ dweight,
+                                                           float* __restrict__ dbias) {
+  __shared__ float sums[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const i64 c = static_cast<i64>(blockIdx.x) * 64 + lane;
+  float s = 0.0f;
+  if (c < 2LL * D) {
+#pragma unroll 4
+    for (int r = wave; r < n; r += 16) s += part[static_cast<i64>(r) * 2 * D + c];
+  }
+  sums[wave][lane] = s;
+  __syncthreads();
+  if (wave != 0 || c >= 2LL * D) return;
+#pragma unroll
+  for (int w = 1; w < 16; ++w) s += sums[w][lane];
+  if (c < D) {
+    if (dweight != nullptr) dweight[c] = s;
+  } else if (dbias != nullptr) {
+    dbias[c - D] = s;
+  }
+}
+
+// ---- launch rules -------------------------------------------------------------------------------
+// waves a row takes: each holds 64 kNormLane columns
+int norm_waves(int D) {
+  int w = 1;
+  while (w <= kNormMaxWaves && w * 64 * kNormLane < D) w *= 2;
+  return w;  // 2 kNormMaxWaves: wider than registers hold
+}
+
+// workgroups of the walk: enough to fill every compute unit, no more than there is work
+unsigned norm_grid(i64 rows, int rows_per_wg, int wgs) {
+  const i64 need = (rows + rows_per_wg - 1) / rows_per_wg;
+  return static_cast<unsigned>(need < wgs ? need : wgs);
+}
+
+constexpr int kNormForwardWgs = 2048;
+constexpr int kNormBackwardWgs = 768;
+
+template <bool XB, bool YB, int VEC, int NCH, int W>
+hipError_t forward_as(const void* x, const float* w, const float* b, float eps, void* y, float* mean, float* rstd,
+                      i64 rows, int D, hipStream_t st) {
+  constexpr int kThreads = W > 4 ? W * 64 : kNormThreads;
+  norm_forward_kernel<XB, YB, VEC, NCH, W><<<norm_grid(rows, kThreads / (64 * W), kNormForwardWgs), kThreads, 0, st>>>(
+      x, w, b, eps, y, mean, rstd, rows, D);
+  return hipGetLastError();
+}
+
+template <bool XB, bool GB, int VEC, int NCH, int W>
+hipError_t backward_as(const void* x, const void* g, const float* mean, const float* rstd, const float* w, void* dx,
+                       float* part, i64 rows, int D, unsigned grid, hipStream_t st) {
+  constexpr int kThreads = W > 4 ? W * 64 : kNormThreads;
+  norm_backward_kernel<XB, GB, VEC, NCH, W><<<grid, kThreads, 0, st>>>(x, g, mean, rstd, w, dx, part, rows, D);
+  return hipGetLastError();
+}
+
+// calls f(waves, chunks) with compile-time values: a narrow row takes one wave and as few chunks
+// of VEC columns as hold it
+template <int VEC, class F>
+hipError_t with_shape(int D, F&& f) {
+  using std::integral_constant;
+  switch (norm_waves(D)) {
+    case 1:
+      if (D <= 64 * kNormLane / 4) return f(integral_constant<int, 1>{}, integral_constant<int, (kNormLane / 4 + VEC - 1) / VEC>{});
+      if (D <= 64 * kNormLane / 2) return f(integral_constant<int, 1>{}, integral_constant<int, kNormLane / 2 / VEC>{});
+      return f(integral_constant<int, 1>{}, integral_constant<int, kNormLane / VEC>{});
+    case 2: return f(integral_constant<int, 2>{}, integral_constant<int, kNormLane / VEC>{});
+    case 4: return f(integral_constant<int, 4>{}, integral_constant<int, kNormLane / VEC>{});
+    case 8: return f(integral_constant<int, 8>{}, integral_constant<int, kNormLane / VEC>{});
+    default: return f(integral_constant<int, 16>{}, integral_constant<int, kNormLane / VEC>{});
+  }
+}
+
+bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <bool XB, bool YB>
+hipError_t forward_typed(const void* x, const float* w, const float* b, float eps, void* y, float* mean, float* rstd,
+                         i64 rows, int D, hipStream_t st) {
+  if (norm_waves(D) > kNormMaxWaves) {
+    norm_forward_wide_kernel<XB, YB><<<norm_grid(rows, 1, 512), 1024, 0, st>>>(x, w, b, eps, y, mean, rstd, rows, D);
+    return hipGetLastError();
+  }
+  constexpr int kVec = XB && YB ? 8 : 4;  // 16 bytes of the wider type
+  if (D % kVec == 0 && at16(x) && at16(y) && at16(w) && at16(b))
+    return with_shape<kVec>(D, [&](auto W, auto NCH) {
+      return forward_as<XB, YB, kVec, NCH.value, W.value>(x, w, b, eps, y, mean, rstd, rows, D, st);
+    });
+  return with_shape<1>(D, [&](auto W, auto NCH) {
+    return forward_as<XB, YB, 1, NCH.value, W.value>(x, w, b, eps, y, mean, rstd, rows, D, st);
+  });
+}
+
+template <bool XB, bool GB>
+hipError_t backward_typed(const void* x, const void* g, const float* mean, const float* rstd, const float* w, void* dx,
+                          float* part, i64 rows, int D, hipStream_t st) {
+  const unsigned grid = static_cast<unsigned>(norm_backward_rows(rows, D));
+  if (norm_waves(D) > kNormMaxWaves) {
+    norm_backward_wide_kernel<XB, GB><<<norm_grid(rows, 1, 512), 1024, 0, st>>>(x, g, mean, rstd, w, dx, rows, D);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || part == nullptr) return e;
+    norm_columns_kernel<XB, GB><<<dim3((D + 255) / 256, grid), 256, 0, st>>>(x, g, mean, rstd, part, rows, D);
+    return hipGetLastError();
+  }
+  constexpr int kVec = XB && GB ? 8 : 4;
+  if (D % kVec == 0 && at16(x) && at16(g) && at16(dx) && at16(w))
+    return with_shape<kVec>(D, [&](auto W, auto NCH) {
+      return backward_as<XB, GB, kVec, NCH.value, W.value>(x, g, mean, rstd, w, dx, part, rows, D, grid, st);
+    });
+  return with_shape<1>(D, [&](auto W, auto NCH) {
+    return backward_as<XB, GB, 1, NCH.value, W.value>(x, g, mean, rstd, w, dx, part, rows, D, grid, st);
+  });
+}
+
+}  // namespace
+
+int norm_backward_rows(i64 rows, int D) {
+  const int waves = norm_waves(D);
+  if (waves > kNormMaxWaves) return static_cast<int>(norm_grid(rows, 1, 64));
+  const int groups = waves > 4 ? 1 : 4 / waves;
+  return static_cast<int>(norm_grid(rows, groups, kNormBackwardWgs));
+}
+
+hipError_t launch_norm_forward(const void* x, bool x_bf16, const float* w, const float* b, float eps, void* y,
+                               bool y_bf16, float* mean, float* rstd, i64 rows, int D, hipStream_t st) {
+  if (rows == 0) return hipSuccess;
+  if (x_bf16) return y_bf16 ? forward_typed<true, true>(x, w, b, eps, y, mean, rstd, rows, D, st)
+                            : forward_typed<true, false>(x, w, b, eps, y, mean, rstd, rows, D, st);
+  return y_bf16 ? forward_typed<false, true>(x, w, b, eps, y, mean, rstd, rows, D, st)
+                : forward_typed<false, false>(x, w, b, eps, y, mean, rstd, rows, D, st);
+}
+
+hipError_t launch_norm_backward(const void* x, bool x_bf16, const void* g, bool g_bf16, const float* mean,
+                                const float* rstd, const float* w, void* dx, float* dweight, float* dbias,
+                                float* part, i64 rows, int D, hipStream_t st) {
+  const bool sums = dweight != nullptr || dbias != nullptr;
+  float* p = sums ? part : nullptr;
+  if (rows > 0) {
+    const hipError_t e =
+        x_bf16 ? (g_bf16 ? backward_typed<true, true>(x, g, mean, rstd, w, dx, p, rows, D, st)
+                         : backward_typed<true, false>(x, g, mean, rstd, w, dx, p, rows, D, st))
+               : (g_bf16 ? backward_typed<false, true>(x, g, mean, rstd, w, dx, p, rows, D, st)
+                         : backward_typed<false, false>(x, g, mean, rstd, w, dx, p, rows, D, st));
+    if (e != hipSuccess) return e;
+  }
+  if (!sums) return hipSuccess;
+  norm_reduce_kernel<<<static_cast<unsigned>((2LL * D + 63) / 64), 1024, 0, st>>>(
+      part, rows > 0 ? norm_backward_rows(rows, D) : 0, D, dweight, dbias);
+  return hipGetLastError();
+}
+
+}  // namespace slstm

@@ -4,6 +4,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace slstm {
@@ -165,6 +167,78 @@ hipError_t launch_gemm_bf16(const void* X, const void* W, const float* bias, flo
                             int N, int K, hipStream_t stream, int splits = 1);
 int gemm_tiles(i64 M, int N);
 int gemm_splits_for(i64 M, int N, int K, int want);
+
+// layer norm of `rows` rows of D columns (k_norm.hip). The backward's `part` holds
+// norm_backward_rows(rows, D) rows of 2 D floats (read only when dweight or dbias is given).
+int norm_backward_rows(i64 rows, int D);
+hipError_t launch_norm_forward(const void* x, bool x_bf16, const float* w, const float* b, float eps, void* y,
+                               bool y_bf16, float* mean, float* rstd, i64 rows, int D, hipStream_t st);
+hipError_t launch_norm_backward(const void* x, bool x_bf16, const void* g, bool g_bf16, const float* mean,
+                                const float* rstd, const float* w, void* dx, float* dweight, float* dbias,
+                                float* part, i64 rows, int D, hipStream_t st);
+
+// ---- linear attention (linear.h, k_linear.hip) ----
+// a (B, T, H, width) operand: strides in elements, the innermost axis dense
+struct LinView {
+  const void* data = nullptr;
+  i64 sb = 0, st = 0, sh = 0;
+};
+// One linear attention of a launch. Widths KD (q, k) and VD (v, out). state_in and state_out are
+// (sequences, H, KD, VD) float32; `transposed`: state_in is stored (.., VD, KD). dot_out, if
+// given, receives out . dot per step, (B, H, T). edge_out: <edge, final state> per sequence and
+// head, edge stored (.., VD, KD).
+struct LinRole {
+  LinView q, k, v, out, dot;
+  const float* state_in = nullptr;
+  float* state_out = nullptr;
+  float* dot_out = nullptr;
+  const float* edge = nullptr;
+  float* edge_out = nullptr;
+  float* seg_states = nullptr;  // n_slots * H states (KD x VD), with more than one segment
+  float* seg_decays = nullptr;  // n_slots * H
+  float o_scale = 1.0f, v_scale = 1.0f;
+  int KD = 0, VD = 0;
+  int reverse = 0, transposed = 0;
+};
+constexpr int kLinMaxRoles = 3;
+struct LinLaunch {
+  LinRole role[kLinMaxRoles];
+  int n_roles = 1;
+  const float* gate = nullptr;
+  i64 gate_b = 0, gate_t = 0, gate_h = 0;
+  const int* cu = nullptr;  // packed sequences (one row), or nullptr
+  int n_seqs = 0;           // sequences: B unpacked
+  int T = 0, H = 0;
+  int seg_len = 0;          // steps of a segment, a multiple of 32
+  int n_seg = 1;            // segments of an unpacked sequence
+  int n_slots = 0;          // (sequence, segment) pairs
+};
+// each segment's own state; a pass whose outputs are in the operands' type; the same with every
+// product in float32 precision
+enum class LinPass { kStates, kForward, kExact };
+int linear_blocks(int width);  // blocks of 32 columns, a power of two
+hipError_t launch_linear_walk(bool bf16, const LinLaunch& a, LinPass pass, hipStream_t st);
+hipError_t launch_linear_join(const LinLaunch& a, hipStream_t st);
+hipError_t launch_linear_keys32(bool bf16, int value_blocks, const LinLaunch& a, LinPass pass, hipStream_t st);
+hipError_t launch_linear_keys64(bool bf16, int value_blocks, const LinLaunch& a, LinPass pass, hipStream_t st);
+hipError_t launch_linear_keys128(bool bf16, int value_blocks, const LinLaunch& a, LinPass pass, hipStream_t st);
+hipError_t launch_linear_keys256(bool bf16, int value_blocks, const LinLaunch& a, LinPass pass, hipStream_t st);
+// dlog_decay (B, T, H) from the inner products r = q . dq and c = k . dk (both (B, H, T)):
+// dg_t = edge + sum over s >= t of r_s - c_s, zero where the decay is zero
+hipError_t launch_linear_gate_gradient(const float* r, const float* c, const float* edge, const LinLaunch& a,
+                                       float* dgate, hipStream_t st);
+// one step: state <- e^g state + k v^T, o = scale state^T q (views without a step axis: st unused)
+struct LinStep {
+  LinView q, k, v;
+  void* out = nullptr;
+  const float* gate = nullptr;
+  i64 gate_b = 0, gate_h = 0;
+  float* state = nullptr;
+  const int* slots = nullptr;
+  int n_slots = 0, B = 0, H = 0, KD = 0, VD = 0;
+  float scale = 1.0f;
+};
+hipError_t launch_linear_step(bool bf16, const LinStep& a, hipStream_t st);
 
 // operand preparation for the weight-gradient products (bfloat16, rounded to nearest even)
 hipError_t launch_transpose_bf16(const void* src, bool src_f32, uint16_t* dst, i64 rows, int cols,

@@ -1,0 +1,195 @@
+"""Linear attention with a decay for each head (the C ABI's slstm_linear_attention_*): a matrix
+memory S (d_key, d_value) per sequence and head,
+
+    S_t = exp(g_t) S_{t-1} + k_t v_t^T,    o_t = scale S_t^T q_t,
+
+as prompts in chunks, as single tokens, and its gradients."""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from .slstm import BF16, F32, _check, _dev, _ptr, _seqs, _shape, _stream, alloc_workspace, load
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
+
+
+def _view(t, name, dtype, shape):
+    """A (..., width) tensor in any order of its leading axes, the last one dense. The stride of an
+    axis of one step is not used and may be anything, so it is not passed on."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    st = [0 if n <= 1 else s for n, s in zip(t.shape, t.stride())]
+    if len(shape) == 3:  # a single step: (B, H, width)
+        return _Heads(t.data_ptr(), st[0], 0, st[1])
+    return _Heads(t.data_ptr(), st[0], st[1], st[2])
+
+
+def _own(t, name):
+    """An output view: no two elements in one place."""
+    if any(s == 0 and n > 1 for n, s in zip(t.shape, t.stride())):
+        raise ValueError(f"{name} must not share elements (a stride of 0)")
+
+
+def _shapes(q, v, steps=True):
+    n = 4 if steps else 3
+    what = "(B, T, n_heads, d)" if steps else "(B, n_heads, d)"
+    for name, t in (("q", q), ("v", v)):
+        if t.dim() != n:
+            raise ValueError(f"{name} must be {what}, got {tuple(t.shape)}")
+    if q.dtype not in _FLOATS:
+        raise TypeError(f"q must be one of {_FLOATS}, got {q.dtype}")
+    return tuple(q.shape), tuple(v.shape[:-1]) + (v.shape[-1],)
+
+
+def _decay(log_decay, lead):
+    """Whether log_decay is one value per head (n_heads) rather than per step and head."""
+    _dev(log_decay, "log_decay", (torch.float32,))
+    per_head = log_decay.dim() == 1
+    _shape(log_decay, "log_decay", (lead[-1],) if per_head else lead)
+    return int(per_head)
+
+
+def _scale(scale, d_key):
+    return float(d_key ** -0.5 if scale is None else scale)
+
+
+def _ref(v):
+    return ctypes.byref(v)
+
+
+def linear_attention_workspace_bytes(B: int, T: int, n_heads: int, d_key: int, d_value: int, n_seqs: int = 0) -> int:
+    return int(load().slstm_linear_attention_workspace_bytes(B, T, n_heads, d_key, d_value, n_seqs))
+
+
+def linear_attention_forward(q, k, v, log_decay, state0=None, scale=None, out=None, final_state=None,
+                             want_final_state=False, cu_seqlens=None, workspace=None, stream=None):
+    """Prompts: o and, if wanted, the final state. q, k (B, T, n_heads, d_key) and v (B, T, n_heads,
+    d_value), float32 or bfloat16, widths multiples of 8 up to 256; any order of the first three
+    axes (slices of a (B, T, 4, d_h) projection, transposed (B, n_heads, T, d) tensors), data and
+    strides in multiples of 16 bytes. log_decay float32, (B, T, n_heads) or, fixed for all steps,
+    (n_heads); -inf starts anew at that step. state0 and final_state (B, n_heads, d_key, d_value)
+    float32. scale: 1 / sqrt(d_key) unless given. Returns (o (B, T, n_heads, d_value) in q's type,
+    final_state or None).
+
+    ``cu_seqlens`` (S + 1 offsets) packs S sequences end to end in one row, as in newton_forward:
+    the states are then (S, n_heads, d_key, d_value)."""
+    L = load()
+    shape, vshape = _shapes(q, v)
+    B, T, H, dk = shape
+    dv = vshape[-1]
+    cu, S = _seqs(cu_seqlens, q)
+    views = [_view(q, "q", q.dtype, shape), _view(k, "k", q.dtype, shape), _view(v, "v", q.dtype, (B, T, H, dv))]
+    per_head = _decay(log_decay, (B, T, H))
+    n = B if cu is None else S
+    if out is None:
+        out = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
+    o = _view(out, "out", q.dtype, (B, T, H, dv))
+    _own(out, "out")
+    if want_final_state and final_state is None:
+        final_state = torch.empty((n, H, dk, dv), dtype=torch.float32, device=q.device)
+    for name, t in (("state0", state0), ("final_state", final_state)):
+        _dev(t, name, (torch.float32,))
+        _shape(t, name, (n, H, dk, dv))
+    need = L.slstm_linear_attention_workspace_bytes(B, T, H, dk, dv, S or 0)
+    if workspace is None and need:
+        workspace = alloc_workspace(need, q.device)
+    status = L.slstm_linear_attention_forward(*map(_ref, views), BF16 if q.dtype == torch.bfloat16 else F32,
+                                              _ptr(log_decay), per_head, _ptr(state0), _scale(scale, dk), _ref(o),
+                                              _ptr(final_state), B, T, H, dk, dv, _ptr(cu), S or 0, _ptr(workspace),
+                                              0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                              _stream(stream))
+    _check(status, "slstm_linear_attention_forward")
+    return out, final_state
+
+
+def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None, out=None, stream=None):
+    """One token: updates ``state`` in place and returns o (B, n_heads, d_value) in q's type. q, k
+    (B, n_heads, d_key), v (B, n_heads, d_value) (strided as in linear_attention_forward), log_decay
+    (B, n_heads) or (n_heads). state (n_slots, n_heads, d_key, d_value) float32; ``slots`` (B) int32
+    names each row's state (a slot outside the pool: the row is skipped, its output zero; no slot
+    twice), without it row b has state b."""
+    L = load()
+    shape, vshape = _shapes(q, v, steps=False)
+    B, H, dk = shape
+    dv = vshape[-1]
+    views = [_view(q, "q", q.dtype, shape), _view(k, "k", q.dtype, shape), _view(v, "v", q.dtype, (B, H, dv))]
+    per_head = _decay(log_decay, (B, H))
+    _dev(state, "state", (torch.float32,))
+    if state.dim() != 4 or tuple(state.shape[1:]) != (H, dk, dv):
+        raise ValueError(f"state must be (n_slots, {H}, {dk}, {dv}), got {tuple(state.shape)}")
+    _dev(slots, "slots", (torch.int32,))
+    _shape(slots, "slots", (B,))
+    if out is None:
+        out = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
+    _dev(out, "out", (q.dtype,))
+    _shape(out, "out", (B, H, dv))
+    status = L.slstm_linear_attention_step(*map(_ref, views), BF16 if q.dtype == torch.bfloat16 else F32,
+                                           _ptr(log_decay), per_head, _ptr(state), _ptr(slots), state.shape[0],
+                                           _scale(scale, dk), _ptr(out), B, H, dk, dv, _stream(stream))
+    _check(status, "slstm_linear_attention_step")
+    return out
+
+
+def linear_attention_backward_workspace_bytes(B: int, T: int, n_heads: int, d_key: int, d_value: int,
+                                              n_seqs: int = 0) -> int:
+    return int(load().slstm_linear_attention_backward_workspace_bytes(B, T, n_heads, d_key, d_value, n_seqs))
+
+
+def linear_attention_backward(q, k, v, log_decay, g_out, state0=None, g_final=None, scale=None, dq=None, dk=None,
+                              dv=None, dlog_decay=None, dstate0=None, want_dlog_decay=None, want_dstate0=False,
+                              cu_seqlens=None, workspace=None, stream=None):
+    """Gradients of linear_attention_forward at the same q, k, v, log_decay, state0 and scale, for
+    the gradients g_out of o (q's type) and g_final of the final state (None: zeros). Returns
+    (dq, dk, dv, dlog_decay or None, dstate0 or None). dq, dk, dv have q's type and may be given as
+    views (slices of one (B, T, 4, d_h) gradient); dlog_decay (B, T, n_heads) float32 is formed
+    unless ``want_dlog_decay`` is False or the decay is fixed per head."""
+    L = load()
+    shape, vshape = _shapes(q, v)
+    B, T, H, d_key = shape
+    d_value = vshape[-1]
+    vshape = (B, T, H, d_value)
+    cu, S = _seqs(cu_seqlens, q)
+    dt = q.dtype
+    per_head = _decay(log_decay, (B, T, H))
+    views = [_view(q, "q", dt, shape), _view(k, "k", dt, shape), _view(v, "v", dt, vshape)]
+    g = _view(g_out, "g_out", dt, vshape)
+    if want_dlog_decay is None:
+        want_dlog_decay = not per_head
+    if want_dlog_decay and dlog_decay is None:
+        dlog_decay = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
+    n = B if cu is None else S
+    if want_dstate0 and dstate0 is None:
+        dstate0 = torch.empty((n, H, d_key, d_value), dtype=torch.float32, device=q.device)
+    for name, t in (("state0", state0), ("g_final", g_final), ("dstate0", dstate0)):
+        _dev(t, name, (torch.float32,))
+        _shape(t, name, (n, H, d_key, d_value))
+    _dev(dlog_decay, "dlog_decay", (torch.float32,))
+    _shape(dlog_decay, "dlog_decay", (B, T, H))
+    dq, dk, dv = (torch.empty(s, dtype=dt, device=q.device) if t is None else t
+                  for t, s in ((dq, shape), (dk, shape), (dv, vshape)))
+    outs = [_view(t, name, dt, s) for name, t, s in (("dq", dq, shape), ("dk", dk, shape), ("dv", dv, vshape))]
+    for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+        _own(t, name)
+    need = L.slstm_linear_attention_backward_workspace_bytes(B, T, H, d_key, d_value, S or 0)
+    if workspace is None:
+        workspace = alloc_workspace(need, q.device)
+    status = L.slstm_linear_attention_backward(*map(_ref, views), BF16 if dt == torch.bfloat16 else F32, _ptr(log_decay),
+                                               per_head, _ptr(state0), _scale(scale, d_key), _ref(g), _ptr(g_final),
+                                               *map(_ref, outs), _ptr(dlog_decay), _ptr(dstate0), B, T, H, d_key,
+                                               d_value, _ptr(cu), S or 0, _ptr(workspace),
+                                               workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(status, "slstm_linear_attention_backward")
+    return dq, dk, dv, dlog_decay, dstate0

@@ -26,7 +26,8 @@ MAX_ITERS = 64
 KERNELS = {"warm_start": 0, "residual_jacobian": 1, "scan_block4": 2, "update": 3,
            "final_residual": 4, "input_projection": 5, "sequential": 6, "newton_iteration": 7,
            "newton_solve": 8, "backward": 9, "weight_gradient": 10, "input_gradient": 11,
-           "head_iteration": 12, "head_sequential": 13, "head_solve": 14, "head_backward": 15}
+           "head_iteration": 12, "head_sequential": 13, "head_solve": 14, "head_backward": 15,
+           "layer_norm": 16, "linear_attention": 17, "linear_step": 18}
 
 EXPORTED = [
     "slstm_status_string", "slstm_last_error", "slstm_newton_workspace_bytes",
@@ -41,6 +42,9 @@ EXPORTED = [
     "slstm_head_sequential_forward", "slstm_head_backward_workspace_bytes", "slstm_head_backward",
     "slstm_head_newton_forward_varlen", "slstm_head_sequential_forward_varlen", "slstm_head_backward_varlen",
     "slstm_newton_forward_noalloc",
+    "slstm_layer_norm_forward", "slstm_layer_norm_backward_workspace_bytes", "slstm_layer_norm_backward",
+    "slstm_linear_attention_workspace_bytes", "slstm_linear_attention_forward", "slstm_linear_attention_step",
+    "slstm_linear_attention_backward_workspace_bytes", "slstm_linear_attention_backward",
 ]
 
 
@@ -75,6 +79,7 @@ class NewtonStats:
 
 _LIB = None
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_i64 = ctypes.c_int64
 
 
 def lib_path() -> str:
@@ -160,6 +165,23 @@ def load(path: str | None = None):
     L.slstm_head_backward_varlen.restype = _i
     L.slstm_head_backward_varlen.argtypes = [_vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp,
                                              _i, _i, _i, _i, _vp, _sz, _vp]
+    L.slstm_layer_norm_forward.restype = _i
+    L.slstm_layer_norm_forward.argtypes = [_vp, _i, _vp, _vp, _f, _vp, _i, _vp, _vp, _i64, _i, _vp]
+    L.slstm_layer_norm_backward_workspace_bytes.restype = _sz
+    L.slstm_layer_norm_backward_workspace_bytes.argtypes = [_i64, _i]
+    L.slstm_layer_norm_backward.restype = _i
+    L.slstm_layer_norm_backward.argtypes = [_vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i, _vp, _sz, _vp]
+    for name in ("slstm_linear_attention_workspace_bytes", "slstm_linear_attention_backward_workspace_bytes"):
+        getattr(L, name).restype = _sz
+        getattr(L, name).argtypes = [_i] * 6
+    L.slstm_linear_attention_forward.restype = _i
+    L.slstm_linear_attention_forward.argtypes = [_vp, _vp, _vp, _i, _vp, _i, _vp, _f, _vp, _vp, _i, _i, _i, _i, _i,
+                                                 _vp, _i, _vp, _sz, _vp]
+    L.slstm_linear_attention_step.restype = _i
+    L.slstm_linear_attention_step.argtypes = [_vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _i, _f, _vp, _i, _i, _i, _i, _vp]
+    L.slstm_linear_attention_backward.restype = _i
+    L.slstm_linear_attention_backward.argtypes = [_vp, _vp, _vp, _i, _vp, _i, _vp, _f, _vp, _vp, _vp, _vp, _vp, _vp,
+                                                  _vp, _i, _i, _i, _i, _i, _vp, _i, _vp, _sz, _vp]
     L.slstm_profile_enable.restype = _i
     L.slstm_profile_enable.argtypes = [_i]
     L.slstm_profile_reset.restype = _i
