@@ -1284,10 +1284,16 @@ slstm_status check_heads_view(const slstm_heads* v, const char* name, slstm_dtyp
 
 slstm::LinView view_of(const slstm_heads* v) { return {v->data, v->stride_b, v->stride_t, v->stride_h}; }
 
-// Segments of the time axis: as many as give every compute unit kLinWgsPerCu workgroups, none
-// shorter than kLinMinSeg steps. One segment needs no pass over k and v before the outputs.
-constexpr int kLinWgsPerCu = 2;
+// Segments of the time axis. A compute unit holds kLinWaves waves of the walk (a workgroup has one
+// for each 32 value columns), so `items` walks cut into n run in ceil(items n / room) rounds of 1 / n
+// of their length each; cutting also reads k and v of all but the last segment once more, at
+// kLinAgain of a walk's time. The rule takes the n with the least sum, segments of kLinMinSeg steps
+// at least. Measured on MI355X (bf16, widths 128): 64 walks of 16384 steps, 256 CUs: 8 segments
+// 0.40 ms, 4 0.46, 2 0.85, 1 0.98; 384 walks of 4096 (a backward call) 1 segment 0.69 ms, 2 0.75, 8 0.83.
+constexpr int kLinWaves = 8;
+constexpr double kLinAgain = 0.6;
 constexpr int kLinMinSeg = 128;
+constexpr int kLinMaxSeg = 64;
 
 struct LinPlan {
   int seg_len, n_seg, n_slots;
@@ -1298,15 +1304,20 @@ struct LinPlan {
 LinPlan linear_plan(int B, int T, int H, int dk, int dv, int n_seqs, int roles) {
   LinPlan p;
   const i64 seqs = n_seqs > 0 ? n_seqs : B;
-  const i64 want = static_cast<i64>(kLinWgsPerCu) * device_cus();
-  const i64 have = seqs * H * roles;
-  i64 n = std::max<i64>(1, (want + have - 1) / have);
-  // packed: sequences of unknown lengths, of which T / seqs is the mean
-  const i64 mean = n_seqs > 0 ? std::max<i64>(1, T / seqs) : T;
-  i64 len = (mean + n - 1) / n;
-  len = std::max<i64>(kLinMinSeg, (len + 31) / 32 * 32);
-  if (n == 1 && n_seqs > 0) len = std::max<i64>(len, 4 * ((mean + 31) / 32 * 32));
-  if (n == 1 && n_seqs == 0) len = std::max<i64>(32, (static_cast<i64>(T) + 31) / 32 * 32);
+  const i64 room = std::max<i64>(1, static_cast<i64>(device_cus()) * kLinWaves / slstm::linear_blocks(std::max(dk, dv)));
+  const i64 items = seqs * H * roles;
+  // Packed sequences: their lengths are on the device. The mean is T / seqs; the rule plans for one of
+  // four times that, and counts the segments of all (a quarter as many, and one more a sequence).
+  const bool packed = n_seqs > 0;
+  const i64 whole = packed ? std::min<i64>(T, 4 * (T / seqs + 1)) : T;
+  i64 n = 1;
+  double best = 0.0;
+  for (i64 m = 1; m <= kLinMaxSeg && (m == 1 || whole / m >= kLinMinSeg); ++m) {
+    const i64 walks = packed ? items + items * m / 4 : items * m;
+    const double cost = (static_cast<double>((walks + room - 1) / room) + kLinAgain * static_cast<double>(m - 1)) / static_cast<double>(m);
+    if (m == 1 || cost < best) best = cost, n = m;
+  }
+  const i64 len = std::max<i64>(32, ((whole + n - 1) / n + 31) / 32 * 32);
   p.seg_len = static_cast<int>(len);
   p.n_seg = static_cast<int>(std::max<i64>(1, (T + len - 1) / len));
   const i64 slots = n_seqs > 0 ? T / len + seqs : seqs * p.n_seg;

@@ -59,12 +59,13 @@ __global__ __launch_bounds__(256) void linear_step_kernel(const LinStep a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = step_load<BF16>(a.v.data, b * a.v.sb + h * a.v.sh + col + e);
     const float d = decay_of(a.gate[b * a.gate_b + h * a.gate_h]);
+    const bool drop = a.gate[b * a.gate_b + h * a.gate_h] <= kZeroDecay;  // whatever the state holds
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       const int row = i * 32 + ry;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[i][e] = fmaf(s[i][e], d, k[i] * v[e]);
+        s[i][e] = drop ? k[i] * v[e] : fmaf(s[i][e], d, k[i] * v[e]);
         o[e] = fmaf(s[i][e], q[i], o[e]);
       }
       if (row < a.KD) *reinterpret_cast<f32x4*>(S + static_cast<i64>(row) * a.VD) = s[i];

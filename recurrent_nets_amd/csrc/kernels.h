@@ -213,8 +213,8 @@ struct LinLaunch {
   int n_seg = 1;            // segments of an unpacked sequence
   int n_slots = 0;          // (sequence, segment) pairs
 };
-// each segment's own state; a pass whose outputs are in the operands' type; the same with every
-// product in float32 precision
+// each segment's own state; the outputs; the same with float32 precision throughout in the roles
+// whose inner products (dot_out) are wanted
 enum class LinPass { kStates, kForward, kExact };
 int linear_blocks(int width);  // blocks of 32 columns, a power of two
 hipError_t launch_linear_walk(bool bf16, const LinLaunch& a, LinPass pass, hipStream_t st);

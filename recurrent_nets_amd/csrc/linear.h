@@ -6,9 +6,15 @@
 // With G_i the sum of g over a chunk's steps up to i, the steps of a chunk of 32 are
 //   o_i = o_s [ e^{G_i} S_0^T q_i + sum_{j <= i} e^{G_i - G_j} (q_i . k_j) v_s v_j ]
 //   S'  = e^{G_31} S_0 + sum_j k_j (e^{G_31 - G_j} v_s v_j)^T.
-// Every exponent is a difference over steps between j and i, never the quotient of two powers.
-// A log decay of kReset or less is a decay of exactly zero in float32: it drops what came before
-// by the index comparison j >= (last reset up to i), so a reset's size never enters G.
+// The state is kept as 2^E S, E (base 2, as G from here on) the decays since it was last scaled:
+//   o_i = o_s 2^(E + G_i) [ S^T q_i + sum_{j <= i} (q_i . k_j) v'_j ],   v'_j = 2^-(E + G_j) v_s v_j
+//   S <- S + sum_j k_j v'_j^T,  E <- E + G_31
+// which needs no exponential per pair of steps and one scaled v for both sums, and scales the state
+// only when |E| passes kMild. Powers of single steps are harmless while |G| is small; where decays
+// are strong, at a reset and at values too large for a factor the chunk is cut into runs of steps,
+// each taken with the others' steps cleared (a rule of decays and values alone, so results do not
+// depend on how time is divided beyond rounding). A log decay of kReset or less is a decay of
+// exactly zero in float32: it drops the state, whatever that holds.
 //
 // The same recurrence, with its operands exchanged, gives the gradients (g the gradient of o,
 // L_t that of S_t):  dq = LA(g, v, k) forward in time on S^T;  dk = LA(v, g, q) and
@@ -19,17 +25,19 @@
 // Layout. One workgroup walks the chunks of one (role, sequence, head, segment of the time axis);
 // wave w owns columns 32 w .. 32 w + 31 of the values, and its part of the state (KD x 32) stays
 // in float32 accumulators of v_mfma_f32_32x32 for the whole walk: lane l holds column l % 32,
-// accumulator r row 8 (r / 4) + 4 (l / 32) + r % 4 of each block of 32 rows. Products contract
-// over an index in any order, so everything is contracted in that order: accumulators r = 8 s ..
-// 8 s + 7 are, converted in place, the operand slice s of the next product (state and scores never
-// pass through LDS), and the other operand is read from LDS as two runs of 4, at 16 s + 4 (l / 32)
-// and 8 further. The scores are formed transposed (rows j, columns i), so that they too are
-// operands where they stand; every wave forms them for itself, which costs 2 KD / 32 of its matrix
-// instructions and saves a barrier and a trip through LDS. Operands with the step index along the
-// registers (k^T, v^T) are read by the transposing LDS load (bf16) or element by element (float32).
+// accumulator r row 8 (r / 4) + 4 (l / 32) + r % 4 of each block of 32 rows. Which key column a row
+// stands for is free, and so is the order in which a product runs over an index: with bits 2 and 3
+// exchanged (lin_swap), accumulators 8 s .. 8 s + 7 hold the 8 consecutive indices from 16 s +
+// 8 (l / 32) on. They are, converted in place, the operand slice s of the next product (state and
+// scores never pass through LDS), whose other operand is then one 16-byte read a lane and slice.
+// The scores are formed transposed (rows j, columns i) for the same reason; every wave forms them
+// for itself, which costs 2 KD / 32 of its matrix instructions and saves a barrier and a trip
+// through LDS. Lanes hold value columns in that order too, so a lane's outputs are runs of 8.
+// Operands with the step index along the registers (k^T, v^T) are read by the transposing LDS load
+// (bf16) or element by element (float32).
 //
 // Tiles of q, k and v are copied global to LDS directly, a stage ahead, one barrier a chunk. LDS
-// rows hold a power of two of bytes; their 16-byte chunks are permuted by row (lin_swizzle) so that
+// rows lie in lines of 128 bytes; their 16-byte chunks are permuted by row (LinTile) so that
 // the 16 rows (or 4 rows by 32 bytes) that the LDS serves together lie on distinct banks. Steps
 // past the end and columns past the width are fetched from outside the buffer's extent: zeros.
 //
@@ -38,8 +46,9 @@
 // operand) is split into NP, NV and NS bf16 terms, 8 bits of the mantissa each. float32 operands
 // use the float32 matrix instructions, with no rounding.
 //
-// Causality holds for what is not finite too: a v_j that is infinite or NaN would reach the
-// chunk's earlier rows as 0 * v_j, so a chunk with one adds its scores row by row.
+// Causality holds for what is not finite too: scores of later steps are cleared, not multiplied by
+// zero, and a step with a v that is infinite or NaN begins a run, so that no earlier row of its
+// chunk meets it.
 #pragma once
 #include "common.h"
 #include "kernels.h"
@@ -58,23 +67,46 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // log decays up to this are a decay of zero: e^-104 is below float32's smallest subnormal
 constexpr float kReset = -104.0f;
 constexpr float kLog2e = 1.44269504088896340736f;
+// Powers of the decays stay within 2^+-kMild in a run of steps and in the state's exponent, values
+// below kTame: a step's own factor 2^-(E + G_j) is then within 2^48, and products of up to 2^80
+// stay finite.
+constexpr float kMild = 24.0f;
+constexpr float kTame = 1.2089258196146292e24f;  // 2^80
 constexpr uint32_t kLinOutside = 0x80000000u;  // a byte offset beyond every buffer extent
 constexpr uint32_t kLinExtent = 0x7fffffffu;
 
 typedef __attribute__((address_space(3))) void* lin_lds_t;
+typedef __attribute__((address_space(3))) unsigned char* lds_bytes;
+template <class T>
+__device__ __forceinline__ T lds_load(lds_bytes p) {
+  return *reinterpret_cast<__attribute__((address_space(3))) T*>(p);
+}
 
 __device__ __forceinline__ rsrc_t lin_rsrc(const void* base) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0),
                                            static_cast<int>(kLinExtent), 0x00020000);
 }
 
-// the permutation of a row's 16-byte chunks for rows of RB bytes
-template <int RB>
-__device__ __forceinline__ uint32_t lin_swizzle(uint32_t row) {
-  constexpr int kShift = RB >= 256 ? 0 : RB == 128 ? 1 : 2;
-  constexpr uint32_t kMask = RB >= 256 ? 7 : RB == 128 ? 3 : 1;
-  return (((row >> kShift) & kMask) << 1) | ((row >> 3) & 1u);
-}
+// bits 2 and 3 exchanged
+__host__ __device__ constexpr uint32_t lin_swap(uint32_t i) { return (i & ~12u) | ((i & 4u) << 1) | ((i & 8u) >> 1); }
+
+// LDS tiles: 32 rows (steps) of a number of columns, as groups of columns of kLine bytes a row. A
+// row's 16-byte chunks are permuted by the row's bits 1 to 3 (lines of 64 bytes: 2 and 3), so that
+// the 16 rows of a slice read, or the 4 rows by 64 bytes of a transposing one, lie on distinct banks;
+// bits 0 and 4, the group and the 64-byte half of a line then only shift an address.
+template <int kRowBytes>
+struct LinTile {
+  static constexpr int kLine = kRowBytes < 128 ? kRowBytes : 128;
+  static_assert(kLine == 64 || kLine == 128, "rows of 64 bytes or of whole lines");
+  static constexpr int kGroup = 32 * kLine;        // bytes of a group
+  static constexpr int kBytes = 32 * kRowBytes;
+  static constexpr int kRows = 1024 / kLine;       // rows of a block, what one wave's load fills
+  static constexpr int kBlocksInGroup = 32 / kRows;
+  static constexpr int kBlocks = kBytes / 1024;
+  static __device__ __forceinline__ uint32_t permute(uint32_t row) {
+    return kLine == 128 ? ((row & 2u) << 1) | ((row & 4u) >> 1) | ((row & 8u) >> 3) : ((row & 4u) >> 1) | ((row & 8u) >> 3);
+  }
+};
 
 __device__ __forceinline__ void lin_barrier() {
   __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's LDS accesses; global loads stay in flight
@@ -82,7 +114,38 @@ __device__ __forceinline__ void lin_barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
-__device__ __forceinline__ void lin_wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+// all but the last N of this wave's memory operations are complete
+template <int N>
+__device__ __forceinline__ void lin_wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+}
+
+// inclusive sums over each half of 32 lanes: shifts within rows of 16, then the first row's sum
+__device__ __forceinline__ float lin_scan32(float v) {
+  auto shifted = [](float x, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  v += shifted(v, std::integral_constant<int, 0x111>{});  // row_shr 1, 2, 4, 8
+  v += shifted(v, std::integral_constant<int, 0x112>{});
+  v += shifted(v, std::integral_constant<int, 0x114>{});
+  v += shifted(v, std::integral_constant<int, 0x118>{});
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xa, 0xf, false));  // row_bcast 15
+  return v;
+}
+
+// the value of lane i of the wave, i the same in every lane
+__device__ __forceinline__ float lane_value(float v, int i) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i));
+}
+
+// all ones where bit i is set, else zero; a value kept where it is set
+__device__ __forceinline__ uint32_t lin_all(uint32_t bits, int i) {
+  return static_cast<uint32_t>(static_cast<int>(bits << (31 - i)) >> 31);
+}
+__device__ __forceinline__ float lin_clear(float v, uint32_t bits, int i) {
+  return __uint_as_float(__float_as_uint(v) & lin_all(bits, i));
+}
 
 // ---- operand slices: 8 values a lane, in the accumulators' row order --------------------------
 template <bool BF16>
@@ -96,35 +159,30 @@ struct LinOps<true> {
   static __device__ __forceinline__ f32x16 mma(const frag& a, const frag& b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
-  // slice s of row `row` of a tile: elements 16 s + 4 half .. + 3 and 16 s + 8 + 4 half .. + 3
-  template <int RB>
-  static __device__ __forceinline__ frag row_slice(const unsigned char* tile, uint32_t row, uint32_t half, int s) {
-    const uint32_t base = row * RB + (lin_swizzle<RB>(row) << 4) + 8 * half;
-    union { u32x2 u[2]; frag f; } r;
-    r.u[0] = *reinterpret_cast<const u32x2*>(tile + (base ^ static_cast<uint32_t>(s << 5)));
-    r.u[1] = *reinterpret_cast<const u32x2*>(tile + (base ^ static_cast<uint32_t>((s << 5) | 16)));
-    return r.f;
+  // slice s of row `row` of a tile: elements 16 s + 8 half .. + 7
+  template <class Tile>
+  static __device__ __forceinline__ frag row_slice(lds_bytes tile, uint32_t row, uint32_t half, int s) {
+    constexpr int kPer = Tile::kLine / 32;  // slices of a group
+    const uint32_t base = row * Tile::kLine + ((Tile::permute(row) ^ half) << 4);
+    return lds_load<frag>(tile + (s / kPer) * Tile::kGroup + (base ^ static_cast<uint32_t>((s % kPer) << 5)));
   }
-  // slice s of column col0 + lane % 32: rows 16 s + 4 half .. + 3 and 16 s + 8 + 4 half .. + 3.
-  // The transposing load gives lane i of 16 the column i of a 4 x 16 block whose rows lanes
-  // 4 r .. 4 r + 3 address, 8 bytes each.
-  template <int RB>
-  static __device__ __forceinline__ frag column_slice(const unsigned char* tile, uint32_t col0, uint32_t lane, int s) {
-    const uint32_t i = lane & 15u, half = lane >> 5;
-    const uint32_t col = col0 + 16u * ((lane >> 4) & 1u) + 4u * (i & 3u);
+  // slice s of column 32 block + lin_swap(lane % 32): rows 16 s + 8 half .. + 7. The transposing load
+  // gives lane i of 16 the column i of a 4 x 16 block whose rows lanes 4 r .. 4 r + 3 address, 8
+  // bytes each; the exchange of bits 2 and 3 is one of the middle two of those four.
+  template <class Tile>
+  static __device__ __forceinline__ frag column_slice(lds_bytes tile, int block, uint32_t lane, int s) {
+    constexpr int kPer = Tile::kLine / 64;  // blocks of 32 columns of a group
+    const uint32_t i = lane & 15u, row = 8u * (lane >> 5) + (i >> 2);
+    const uint32_t at = lin_swap(4u * (i & 3u));  // of the 16 columns
+    const uint32_t base = row * Tile::kLine + (((((lane & 16u) + at) >> 3) ^ Tile::permute(row)) << 4) + 2u * (at & 7u);
+    const uint32_t side = static_cast<uint32_t>((block % kPer) << 6);
+    const lds_bytes group = tile + (block / kPer) * Tile::kGroup + s * 16 * Tile::kLine;
     union { s16x4 v[2]; frag f; } r;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t row = 16u * s + 8u * e + 4u * half + (i >> 2);
-      const uint32_t at = row * RB + (((col >> 3) ^ lin_swizzle<RB>(row)) << 4) + 2u * (col & 7u);
-      r.v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) s16x4*)(const_cast<unsigned char*>(tile) + at));
-    }
+    for (int e = 0; e < 2; ++e)
+      r.v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) s16x4*>(
+          group + e * 4 * Tile::kLine + (base ^ side ^ static_cast<uint32_t>(e << 5))));
     return r.f;
-  }
-  static __device__ __forceinline__ float element(const unsigned char* tile, int RB, uint32_t swizzle, uint32_t row,
-                                                  uint32_t col) {
-    return bf16_to_f32(*reinterpret_cast<const uint16_t*>(tile + row * RB + (((col >> 3) ^ swizzle) << 4) + 2u * (col & 7u)));
   }
   static __device__ __forceinline__ f32x8 widen(const frag& f) {
     union { frag f; uint32_t u[4]; } r{f};
@@ -136,36 +194,58 @@ struct LinOps<true> {
     }
     return v;
   }
-  // v as N bf16 terms, each the rounding of what the ones before it leave
+  // the elements whose bits are set, zeros elsewhere
+  static __device__ __forceinline__ frag keep(frag f, uint32_t bits) {
+    return apply(f, mask_of(bits));
+  }
+  // v as N bf16 terms, each the rounding of what the ones before it leave. What is left of a pair's
+  // values is formed by the two-term dot product with (-1, 0) and (0, -1), exact as a difference of
+  // nearby numbers: one instruction a value, where widening first would take two.
   template <int N>
   static __device__ __forceinline__ void split(f32x8 v, frag (&out)[N]) {
+    union { uint32_t u; bf16x2 b; } first, second;
+    // kept in registers: as constants the compiler would encode them as operands of another type
+    if constexpr (N > 1) {
+      asm("v_mov_b32 %0, 0xbf80" : "=v"(first.u));
+      asm("v_mov_b32 %0, 0xbf800000" : "=v"(second.u));
+    }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       out[n] = __builtin_convertvector(v, frag);
-      if (n + 1 < N) v -= widen(out[n]);
+      if (n + 1 < N) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bf16x2 pair = {out[n][2 * i], out[n][2 * i + 1]};
+          v[2 * i] = __builtin_amdgcn_fdot2_f32_bf16(pair, first.b, v[2 * i], false);
+          v[2 * i + 1] = __builtin_amdgcn_fdot2_f32_bf16(pair, second.b, v[2 * i + 1], false);
+        }
+      }
     }
   }
-  // whether a slice holds an infinity or NaN
-  static __device__ __forceinline__ bool not_finite(const frag& f) {
-    union { frag f; uint32_t u[4]; } r{f};
-    bool bad = false;
+  // keep() as a mask made once
+  typedef u32x4 mask;
+  static __device__ __forceinline__ mask mask_of(uint32_t bits) {
+    mask m;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      bad |= (r.u[i] & 0x7f800000u) == 0x7f800000u || (r.u[i] & 0x7f80u) == 0x7f80u;
-    return bad;
+    for (int i = 0; i < 4; ++i) m[i] = (lin_all(bits, 2 * i) & 0xffffu) | (lin_all(bits, 2 * i + 1) << 16);
+    return m;
   }
-  // 4 values of a row of global memory at a byte offset, and back
-  static __device__ __forceinline__ f32x4 load4(rsrc_t r, uint32_t off) {
-    const u32x2 u = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
-    return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                 __uint_as_float(u.y & 0xffff0000u)};
+  static __device__ __forceinline__ frag apply(frag f, mask m) {
+    union { frag f; u32x4 u; } r{f};
+    r.u &= m;
+    return r.f;
   }
-  typedef u32x2 packed4;
-  static __device__ __forceinline__ packed4 pack4(float a, float b, float c, float d) {
-    return u32x2{pack_bf16(a, b), pack_bf16(c, d)};
+  // 8 values of a row of global memory at a byte offset, and back
+  typedef frag packed8;
+  static __device__ __forceinline__ packed8 load8(rsrc_t r, uint32_t off) {
+    union { u32x4 u; frag f; } v{__builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0)};
+    return v.f;
   }
-  static __device__ __forceinline__ void store4(packed4 v, rsrc_t r, uint32_t off) {
-    __builtin_amdgcn_raw_buffer_store_b64(v, r, off, 0, 0);
+  static __device__ __forceinline__ f32x8 unpack8(packed8 v) { return widen(v); }
+  static __device__ __forceinline__ packed8 pack8(f32x8 v) { return __builtin_convertvector(v, frag); }
+  static __device__ __forceinline__ void store8(packed8 v, rsrc_t r, uint32_t off) {
+    union { frag f; u32x4 u; } t{v};
+    __builtin_amdgcn_raw_buffer_store_b128(t.u, r, off, 0, 0);
   }
 };
 
@@ -179,50 +259,54 @@ struct LinOps<false> {
     for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
     return c;
   }
-  template <int RB>
-  static __device__ __forceinline__ frag row_slice(const unsigned char* tile, uint32_t row, uint32_t half, int s) {
-    const uint32_t base = row * RB, sw = lin_swizzle<RB>(row);
+  template <class Tile>
+  static __device__ __forceinline__ frag row_slice(lds_bytes tile, uint32_t row, uint32_t half, int s) {
+    const uint32_t base = row * Tile::kLine + ((Tile::permute(row) ^ (2u * half)) << 4);
+    const lds_bytes group = tile + (s >> 1) * Tile::kGroup;
     union { f32x4 v[2]; frag f; } r;
-    r.v[0] = *reinterpret_cast<const f32x4*>(tile + base + (((4u * s + half) ^ sw) << 4));
-    r.v[1] = *reinterpret_cast<const f32x4*>(tile + base + (((4u * s + 2u + half) ^ sw) << 4));
+    r.v[0] = lds_load<f32x4>(group + (base ^ static_cast<uint32_t>((s & 1) << 6)));
+    r.v[1] = lds_load<f32x4>(group + (base ^ static_cast<uint32_t>((s & 1) << 6 | 16)));
     return r.f;
   }
-  template <int RB>
-  static __device__ __forceinline__ frag column_slice(const unsigned char* tile, uint32_t col0, uint32_t lane, int s) {
-    const uint32_t half = lane >> 5, col = col0 + (lane & 31u);
+  template <class Tile>
+  static __device__ __forceinline__ frag column_slice(lds_bytes tile, int block, uint32_t lane, int s) {
+    const uint32_t row = 8u * (lane >> 5), col = lin_swap(lane & 31u);
+    const uint32_t base = row * Tile::kLine + (((col >> 2) ^ Tile::permute(row)) << 4) + 4u * (col & 3u);
+    const lds_bytes group = tile + block * Tile::kGroup + s * 16 * Tile::kLine;
     frag f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t row = 16u * s + 8u * (e >> 2) + 4u * half + (e & 3);
-      f[e] = *reinterpret_cast<const float*>(tile + row * RB + (((col >> 2) ^ lin_swizzle<RB>(row)) << 4) + 4u * (col & 3u));
-    }
+    for (int e = 0; e < 8; ++e)
+      f[e] = lds_load<float>(group + e * Tile::kLine + (base ^ static_cast<uint32_t>((e & 2) << 5 | (e & 4) << 3)));
     return f;
   }
-  static __device__ __forceinline__ float element(const unsigned char* tile, int RB, uint32_t swizzle, uint32_t row,
-                                                  uint32_t col) {
-    return *reinterpret_cast<const float*>(tile + row * RB + (((col >> 2) ^ swizzle) << 4) + 4u * (col & 3u));
-  }
   static __device__ __forceinline__ f32x8 widen(const frag& f) { return f; }
+  // keep() as a mask made once
+  typedef uint32_t mask;
+  static __device__ __forceinline__ mask mask_of(uint32_t bits) { return bits; }
+  static __device__ __forceinline__ frag apply(frag f, mask m) { return keep(f, m); }
+  static __device__ __forceinline__ frag keep(frag f, uint32_t bits) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = lin_clear(f[e], bits, e);
+    return f;
+  }
   template <int N>
   static __device__ __forceinline__ void split(f32x8 v, frag (&out)[N]) {
     static_assert(N == 1, "float32 operands are not split");
     out[0] = v;
   }
-  static __device__ __forceinline__ bool not_finite(const frag& f) {
-    bool bad = false;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) bad |= (__float_as_uint(f[e]) & 0x7f800000u) == 0x7f800000u;
-    return bad;
-  }
-  static __device__ __forceinline__ f32x4 load4(rsrc_t r, uint32_t off) {
-    union { u32x4 u; f32x4 f; } v{__builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0)};
+  static __device__ __forceinline__ f32x8 load8(rsrc_t r, uint32_t off) {
+    union { u32x4 u[2]; f32x8 f; } v;
+    v.u[0] = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+    v.u[1] = __builtin_amdgcn_raw_buffer_load_b128(r, off, 16, 0);
     return v.f;
   }
-  typedef f32x4 packed4;
-  static __device__ __forceinline__ packed4 pack4(float a, float b, float c, float d) { return f32x4{a, b, c, d}; }
-  static __device__ __forceinline__ void store4(packed4 v, rsrc_t r, uint32_t off) {
-    union { f32x4 f; u32x4 u; } t{v};
-    __builtin_amdgcn_raw_buffer_store_b128(t.u, r, off, 0, 0);
+  typedef f32x8 packed8;
+  static __device__ __forceinline__ packed8 pack8(f32x8 v) { return v; }
+  static __device__ __forceinline__ f32x8 unpack8(packed8 v) { return v; }
+  static __device__ __forceinline__ void store8(packed8 v, rsrc_t r, uint32_t off) {
+    union { f32x8 f; u32x4 u[2]; } t{v};
+    __builtin_amdgcn_raw_buffer_store_b128(t.u[0], r, off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(t.u[1], r, off, 16, 0);
   }
 };
 
@@ -249,11 +333,15 @@ __device__ __forceinline__ bool lin_item(const LinLaunch& a, int slot, int head,
     return true;
   }
   auto first = [&](int s) { return min(max(a.cu[s], 0), a.T); };
-  int lo = 0, hi = a.n_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first(mid) / a.seg_len + mid <= slot) lo = mid;
-    else hi = mid - 1;
+  // the last sequence whose slots begin at or before this one: the 64 lanes look at once
+  int lo = 0, n = a.n_seqs;
+  while (n > 1) {
+    const int stride = (n + 63) / 64;
+    const int s = lo + static_cast<int>(threadIdx.x & 63) * stride;
+    const bool before = s < lo + n && first(s) / a.seg_len + s <= slot;
+    const int last = 63 - __clzll(static_cast<long long>(__ballot(before) | 1ull));
+    n = min(stride, n - last * stride);
+    lo += last * stride;
   }
   it.seq = lo;
   it.start = first(lo);
@@ -263,328 +351,470 @@ __device__ __forceinline__ bool lin_item(const LinLaunch& a, int slot, int head,
   return it.seg >= 0 && (it.seg == 0 || it.seg < (it.len + a.seg_len - 1) / a.seg_len);
 }
 
+// a type as an argument
+template <class T>
+struct lin_type {
+  typedef T type;
+};
+
 // ---- the walk ------------------------------------------------------------------------------------
-// KB, VB: blocks of 32 columns of keys and values (powers of two: LDS rows). kFull: outputs and
-// final states; otherwise only each segment's own contribution to the state and its decay.
-template <bool BF16, int KB, int VB, bool kFull, int NS, int NP, int NV>
-__global__ __launch_bounds__(64 * VB, 2) void linear_walk_kernel(const LinLaunch a) {
+// KB, VB: blocks of 32 columns of keys and values (powers of two).
+// LDS of a workgroup: two stages where it holds them (two objects: the compiler then sees which one is
+// being filled), the steps' factors of v (a copy a wave) and the waves' parts of inner products
+template <bool BF16, int KB, int VB, bool kFull>
+struct LinShape {
+  typedef LinOps<BF16> Ops;
+  typedef LinTile<KB * 32 * Ops::kSize> TileK;
+  typedef LinTile<VB * 32 * Ops::kSize> TileV;
+  static constexpr int kStage = (kFull ? 2 : 1) * TileK::kBytes + TileV::kBytes;
+  static constexpr int kStages = 2 * kStage <= 152 * 1024 ? 2 : 1;
+  static __device__ __forceinline__ lds_bytes stage0() {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[kStage];
+    return (lds_bytes)lds;
+  }
+  static __device__ __forceinline__ lds_bytes stage1() {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[kStages > 1 ? kStage : 16];
+    return (lds_bytes)lds;
+  }
+  static __device__ __forceinline__ float (&scales())[VB][32] {
+    __shared__ __attribute__((aligned(16))) float lds[VB][32];
+    return lds;
+  }
+  static __device__ __forceinline__ float (&dots())[2][VB][32] {
+    __shared__ float lds[2][VB][32];
+    return lds;
+  }
+};
+
+// kFull: outputs and final states; otherwise only each segment's own contribution to the state and
+// its decay. kDots: the outputs' inner products.
+template <bool BF16, int KB, int VB, bool kFull, bool kDots, int NS, int NP, int NV>
+__device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R, const LinItem& it) {
+  typedef LinShape<BF16, KB, VB, kFull> Shape;
+  const lds_bytes st0 = Shape::stage0();
+  const lds_bytes st1 = Shape::stage1();
+  auto& scales = Shape::scales();
+  auto& dots = Shape::dots();
   typedef LinOps<BF16> Ops;
   typedef typename Ops::frag frag;
+  typedef typename Shape::TileK TileK;
+  typedef typename Shape::TileV TileV;
   constexpr int kSize = Ops::kSize;
-  constexpr int RBK = KB * 32 * kSize, RBV = VB * 32 * kSize;
-  constexpr int kTileK = 32 * RBK, kTileV = 32 * RBV;
-  constexpr int kStage = (kFull ? 2 : 1) * kTileK + kTileV;
-  // two stages where LDS holds them (as two objects: the compiler then sees which one is being filled)
-  constexpr bool kTwo = 2 * kStage <= 144 * 1024;
-  __shared__ __attribute__((aligned(1024))) unsigned char st0[kStage];
-  __shared__ __attribute__((aligned(1024))) unsigned char st1[kTwo ? kStage : 16];
-  __shared__ __attribute__((aligned(16))) float gates[VB][2][32];  // G_j and the weights w_j, a copy a wave
-  __shared__ float dots[2][VB][32];
-
+  constexpr int kTileK = TileK::kBytes, kTileV = TileV::kBytes;
+  constexpr int kStages = Shape::kStages;
   const int lane = threadIdx.x & 63;
   const int wave = VB == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t half = static_cast<uint32_t>(lane) >> 5, li = static_cast<uint32_t>(lane) & 31u;
-
-  // workgroup -> (role, head, slot): the roles of an item follow each other on the same XCD
-  const int bid = blockIdx.x;
-  const int n_items = a.n_slots * a.H;
-  int role, item;
-  if (a.n_roles == 1) {
-    role = 0;
-    item = bid;
-  } else {
-    const int xcd = bid & 7, idx = bid >> 3;
-    role = idx % a.n_roles;
-    item = (idx / a.n_roles) * 8 + xcd;
-  }
-  if (item >= n_items) return;
-  LinItem it;
-  if (!lin_item(a, item / a.H, item % a.H, it)) return;
-  const LinRole& R = a.role[role];
   const int KD = R.KD, VD = R.VD;
+  // kept (as values of a lane), where the compiler would read the arguments again in every chunk
+  const float o_scale = lane_value(R.o_scale, 0), v_scale = lane_value(R.v_scale, 0);
   const int p_begin = it.seg * a.seg_len;
   const int p_end = min(it.len, p_begin + a.seg_len);
   const int n_chunks = max(0, (p_end - p_begin + 31) >> 5);
   if (!kFull && p_end >= it.len) return;  // nothing follows a sequence's last segment
 
-  const i64 item_q = it.row * R.q.sb + it.start * R.q.st + it.head * R.q.sh;
-  const i64 item_k = it.row * R.k.sb + it.start * R.k.st + it.head * R.k.sh;
-  const i64 item_v = it.row * R.v.sb + it.start * R.v.st + it.head * R.v.sh;
+  // Tiles are addressed from the lowest step of their chunk: forward in time the step of the row 0,
+  // backward that of row 31, which in a sequence's last chunk may lie before its first step (rows
+  // past the end are never fetched). The address moves by 32 steps a chunk, a lane's offsets stay.
+  const int low = R.reverse ? it.len - 32 - p_begin : p_begin;
+  const int turn = R.reverse ? -32 : 32;
+  auto at_first = [&](const LinView& v) {
+    return static_cast<const char*>(v.data) +
+           (it.row * v.sb + (static_cast<i64>(it.start) + low) * v.st + it.head * v.sh) * kSize;
+  };
+  auto row_step = [&](int r) { return R.reverse ? 31 - r : r; };
 
-  // lowest step of the chunk at position p0, and the step of its row r relative to that
-  auto low_step = [&](int p0) { return R.reverse ? max(it.len - 32 - p0, 0) : p0; };
-  auto row_step = [&](int p0, int r) { return R.reverse ? it.len - 1 - p0 - r - max(it.len - 32 - p0, 0) : r; };
-
-  // one tile: 1 KiB blocks (1024 / RB rows) dealt to the waves; lane l fills slot l % (RB / 16) of
-  // its block's row, that is, fetches the chunk which the permutation puts there
-  auto issue_tile = [&](const LinView& v, i64 item_off, int width, int p0, unsigned char* dst, auto rb) {
-    constexpr int RB = decltype(rb)::value;
-    constexpr int kChunks = RB / 16;
-    constexpr int kBlocks = 32 * RB / 1024;
-    const rsrc_t r = lin_rsrc(static_cast<const char*>(v.data) + (item_off + static_cast<i64>(low_step(p0)) * v.st) * kSize);
+  // one tile: blocks of 1 KiB dealt to the waves, block i VB + wave. A lane fills one chunk of one row
+  // of its block, that is, fetches the one which the permutation puts there; its offset is the same
+  // in every block but for the row's bit 3 (odd blocks of a group).
+  auto lane_offset = [&](const LinView& v, int odd, auto tile) {
+    typedef typename decltype(tile)::type Tile;
+    constexpr uint32_t kChunks = Tile::kLine / 16;
+    const uint32_t row = static_cast<uint32_t>(lane) / kChunks;
+    const uint32_t c = (static_cast<uint32_t>(lane) % kChunks) ^ Tile::permute(row + static_cast<uint32_t>(odd) * Tile::kRows);
+    return static_cast<uint32_t>(R.reverse ? Tile::kRows - 1 - row : row) * static_cast<uint32_t>(v.st * kSize) + c * 16u;
+  };
+  const lin_type<TileK> tile_k{};
+  const lin_type<TileV> tile_v{};
+  constexpr int kOdd = VB == 1 ? 2 : 1;  // with more waves a wave's blocks are all odd or all even
+  const char *base_q = nullptr, *base_k = at_first(R.k), *base_v = at_first(R.v);
+  const i64 turn_k = static_cast<i64>(turn) * R.k.st * kSize, turn_v = static_cast<i64>(turn) * R.v.st * kSize;
+  i64 turn_q = 0;
+  uint32_t off_q[kOdd], off_k[kOdd], off_v[kOdd];
 #pragma unroll
-    for (int i = 0; i < (kBlocks + VB - 1) / VB; ++i) {
-      const int blk = i * VB + wave;
-      if (kBlocks % VB != 0 && blk >= kBlocks) break;
-      const uint32_t row = static_cast<uint32_t>(blk * (1024 / RB)) + static_cast<uint32_t>(lane) / kChunks;
-      const uint32_t c = (static_cast<uint32_t>(lane) % kChunks) ^ lin_swizzle<RB>(row);
-      const int col = static_cast<int>(c) * (16 / kSize);
-      const bool in = p0 + static_cast<int>(row) < p_end && col < width;
-      const uint32_t off = in ? static_cast<uint32_t>(row_step(p0, static_cast<int>(row))) * static_cast<uint32_t>(v.st * kSize) + col * kSize
-                              : kLinOutside;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lin_lds_t)(dst + blk * 1024), 16, off, 0, 0, 0);
+  for (int i = 0; i < kOdd; ++i) {
+    off_k[i] = lane_offset(R.k, (i + wave) & 1, tile_k);
+    off_v[i] = lane_offset(R.v, (i + wave) & 1, tile_v);
+    if constexpr (kFull) off_q[i] = lane_offset(R.q, (i + wave) & 1, tile_k);
+  }
+  if constexpr (kFull) {
+    base_q = at_first(R.q);
+    turn_q = static_cast<i64>(turn) * R.q.st * kSize;
+  }
+  // `rows`: the chunk's steps (fewer than 32 in a segment's last one)
+  auto fetch = [&](const char* base, const LinView& v, const uint32_t (&off)[kOdd], int rows, int width, lds_bytes dst, auto tile) {
+    typedef typename decltype(tile)::type Tile;
+    constexpr uint32_t kChunks = Tile::kLine / 16;
+    const rsrc_t r = lin_rsrc(base);
+    const uint32_t step_bytes = static_cast<uint32_t>(v.st * kSize);
+    const bool plain = rows >= 32 && width * kSize * 32 == Tile::kBytes;
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      if (plain != (pass == 0)) continue;
+#pragma unroll
+      for (int i = 0; i < (Tile::kBlocks + VB - 1) / VB; ++i) {
+        const int blk = i * VB + wave;
+        if (Tile::kBlocks % VB != 0 && blk >= Tile::kBlocks) break;
+        const int group = blk / Tile::kBlocksInGroup, part = blk % Tile::kBlocksInGroup;
+        const uint32_t shift = static_cast<uint32_t>(R.reverse ? Tile::kBlocksInGroup - 1 - part : part) * Tile::kRows * step_bytes +
+                               static_cast<uint32_t>(group * Tile::kLine);
+        uint32_t o = off[i & (kOdd - 1)];
+        if (pass == 1) {
+          const uint32_t row = static_cast<uint32_t>(lane) / kChunks + static_cast<uint32_t>(part * Tile::kRows);
+          const uint32_t c = (static_cast<uint32_t>(lane) % kChunks) ^ Tile::permute(row);
+          const bool in = static_cast<int>(row) < rows && group * Tile::kLine + static_cast<int>(c) * 16 < width * kSize;
+          o = in ? o : kLinOutside;
+        }
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lin_lds_t)(dst + blk * 1024), 16, o, shift, 0, 0);
+      }
     }
   };
-  auto issue = [&](unsigned char* stg, int p0) {
-    issue_tile(R.k, item_k, KD, p0, stg, std::integral_constant<int, RBK>{});
-    issue_tile(R.v, item_v, VD, p0, stg + kTileK, std::integral_constant<int, RBV>{});
-    if constexpr (kFull) issue_tile(R.q, item_q, KD, p0, stg + kTileK + kTileV, std::integral_constant<int, RBK>{});
+  auto issue = [&](lds_bytes stg, int rows) {
+    fetch(base_k, R.k, off_k, rows, KD, stg, tile_k);
+    fetch(base_v, R.v, off_v, rows, VD, stg + kTileK, tile_v);
+    base_k += turn_k;
+    base_v += turn_v;
+    if constexpr (kFull) {
+      fetch(base_q, R.q, off_q, rows, KD, stg + kTileK + kTileV, tile_k);
+      base_q += turn_q;
+    }
   };
-  // log decay entering position p (in base 2), 0 past the end; backward in time the step after it
+  // log decay entering position p0 + li, 0 past the end; backward in time that of the step after it
+  // (0 at the first position)
   const float* gate = a.gate + it.row * a.gate_b + it.start * a.gate_t + it.head * a.gate_h;
-  auto load_gate = [&](int p) -> float {
-    if (p >= p_end || (R.reverse && p == 0)) return 0.0f;
-    const int step = R.reverse ? it.len - p : p;
-    return gate[step * a.gate_t];
+  const char* base_g = reinterpret_cast<const char*>(gate + (static_cast<i64>(low) + (R.reverse ? 1 : 0)) * a.gate_t);
+  const i64 turn_g = static_cast<i64>(turn) * a.gate_t * 4;
+  const uint32_t off_g = static_cast<uint32_t>(row_step(static_cast<int>(li))) * static_cast<uint32_t>(a.gate_t * 4);
+  auto load_gate = [&](int p0) -> float {
+    const bool in = p0 + static_cast<int>(li) < p_end && !(R.reverse && p0 + static_cast<int>(li) == 0);
+    const float g = buf_ld(lin_rsrc(base_g), in ? off_g : kLinOutside, 0);
+    base_g += turn_g;
+    return g;
   };
 
   // ---- the state this segment starts from ----
-  const int col = wave * 32 + static_cast<int>(li);
+  const int col = wave * 32 + static_cast<int>(lin_swap(li));
   f32x16 S[KB];
   const float* from = nullptr;
-  i64 rs = VD, cs = 1;
+  int rs = VD, cs = 1;
   if (kFull && it.seg > 0) {
     from = R.seg_states + (static_cast<i64>(it.slot - 1) * a.H + it.head) * KD * VD;
   } else if (kFull && R.state_in != nullptr) {
     from = R.state_in + (static_cast<i64>(it.seq) * a.H + it.head) * KD * VD;
     if (R.transposed) rs = 1, cs = KD;
   }
+  // (loads that fall outside the buffer are zeros: all are issued before the first is waited for)
+  const rsrc_t r_from = lin_rsrc(from);
+  const bool has = from != nullptr && col < VD;
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const int k = kb * 32 + 8 * (r >> 2) + 4 * static_cast<int>(half) + (r & 3);
-      S[kb][r] = (from != nullptr && k < KD && col < VD) ? from[k * rs + col * cs] : 0.0f;
+      const int k = kb * 32 + 16 * (r >> 3) + 8 * static_cast<int>(half) + (r & 7);
+      S[kb][r] = buf_ld(r_from, has && k < KD ? static_cast<uint32_t>(k * rs + col * cs) * 4u : kLinOutside, 0);
     }
+  float E = 0.0f;  // the state is 2^E S
   float seg_decay = 1.0f;
 
-  typename Ops::packed4 held[4];  // the chunk's outputs, stored after the next barrier
-  const i64 item_o = kFull ? it.row * R.out.sb + it.start * R.out.st + it.head * R.out.sh : 0;
-  auto store_held = [&](int p0) {
-    const rsrc_t r = lin_rsrc(static_cast<const char*>(R.out.data) + (item_o + static_cast<i64>(low_step(p0)) * R.out.st) * kSize);
+  // outputs: a lane holds 2 runs of 8 columns of a step
+  const char* base_o = nullptr;
+  i64 turn_o = 0;
+  uint32_t off_o[2];
+  auto output_offset = [&](const LinView& v, int i) {
+    const int c = wave * 32 + 16 * i + 8 * static_cast<int>(half);
+    return c < VD ? static_cast<uint32_t>(row_step(static_cast<int>(li))) * static_cast<uint32_t>(v.st * kSize) + c * kSize : kLinOutside;
+  };
+  if constexpr (kFull) {
+    base_o = at_first(R.out);
+    turn_o = static_cast<i64>(turn) * R.out.st * kSize;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) off_o[i] = output_offset(R.out, i);
+  }
+  // their inner products with R.dot's rows, whose loads are issued before those of the tiles ahead
+  // (a wait for them would else wait for those too); the waves' parts meet after the next barrier
+  const char* base_d = nullptr;
+  i64 turn_d = 0;
+  uint32_t off_d[2];
+  typename Ops::packed8 dot_in[2];
+  float* dot_row = nullptr;
+  if constexpr (kDots) {
+    if (R.dot_out != nullptr) {
+      base_d = at_first(R.dot);
+      turn_d = static_cast<i64>(turn) * R.dot.st * kSize;
+      dot_row = R.dot_out + (it.row * a.H + it.head) * static_cast<i64>(a.T) + it.start;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) off_d[i] = output_offset(R.dot, i);
+  }
+  auto load_dots = [&](int p0) {
+    if (dot_row == nullptr) return;
+    const rsrc_t r = lin_rsrc(base_d);
+    base_d += turn_d;
     const bool in = p0 + static_cast<int>(li) < p_end;
-    const uint32_t row_off = static_cast<uint32_t>(row_step(p0, static_cast<int>(li))) * static_cast<uint32_t>(R.out.st * kSize);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = wave * 32 + 8 * i + 4 * static_cast<int>(half);
-      Ops::store4(held[i], r, in && c < VD ? row_off + c * kSize : kLinOutside);
-    }
-    // the inner products of the outputs with R.dot's rows, the waves' parts in order
-    if (R.dot_out != nullptr && wave == 0 && lane < 32 && in) {
-      float s = 0.0f;
+    for (int i = 0; i < 2; ++i) dot_in[i] = Ops::load8(r, in ? off_d[i] : kLinOutside);
+  };
+  auto store_dots = [&](int p0) {
+    if (dot_row == nullptr || wave != 0 || lane >= 32 || p0 + lane >= p_end) return;
+    float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < VB; ++w) s += dots[(p0 >> 5) & 1][w][lane];
-      const int step = low_step(p0) + row_step(p0, lane);
-      R.dot_out[(it.row * a.H + it.head) * static_cast<i64>(a.T) + it.start + step] = s;
-    }
+    for (int w = 0; w < VB; ++w) s += dots[(p0 >> 5) & 1][w][lane];
+    dot_row[R.reverse ? it.len - 1 - p0 - lane : p0 + lane] = s;
   };
 
-  auto chunk = [&](unsigned char* stg, int p0, float g) {
-    const unsigned char* tk = stg;
-    const unsigned char* tv = stg + kTileK;
-    const unsigned char* tq = stg + kTileK + kTileV;
-    // ---- decays of the chunk: lanes li = i hold G_i; copies for the rows j through LDS ----
+  // A chunk is one run of steps as a rule. A run ends before a step whose decays since the run's
+  // first one leave 2^+-kMild, before a reset and before a step with values of kTame or more (or not
+  // finite: those then reach no earlier row); what remains is taken as further runs.
+  constexpr int kSlices = 2 * KB;
+  typename Ops::mask earlier[2];  // of the scores of step i = li: steps j <= i
+#pragma unroll
+  for (int s = 0; s < 2; ++s) earlier[s] = Ops::mask_of((0xffffffffu >> (31u - li)) >> (16 * s + 8 * half));
+  auto chunk = [&](lds_bytes stg, int p0, float g) {
+    const lds_bytes tk = stg;
+    const lds_bytes tv = stg + kTileK;
+    const lds_bytes tq = stg + kTileK + kTileV;
     const uint32_t resets = static_cast<uint32_t>(__ballot(g <= kReset));
-    float G = g <= kReset ? 0.0f : g * kLog2e;
+    const float g2 = g <= kReset ? 0.0f : g * kLog2e;
+    const float G = lin_scan32(g2);
+    int first = 0;
+    do {
+      frag vt[2];
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const float up = __shfl_up(G, off, 32);
-      if (li >= static_cast<uint32_t>(off)) G += up;
-    }
-    const uint32_t upto = resets & (0xffffffffu >> (31u - li));
-    const int since = 31 - __clz(static_cast<int>(upto));  // last reset up to i, -1 without one
-    const int since_end = 31 - __clz(static_cast<int>(resets));
-    const float G_end = __shfl(G, 31, 32);
-    const float w = static_cast<int>(li) >= since_end ? __builtin_amdgcn_exp2f(G_end - G) * R.v_scale : 0.0f;
-    const float decay = since_end >= 0 ? 0.0f : __builtin_amdgcn_exp2f(G_end);
-    if (lane < 32) {
-      gates[wave][0][lane] = G;
-      gates[wave][1][lane] = w;
-    }
-    __builtin_amdgcn_wave_barrier();
-    float wj[16];
+      for (int s = 0; s < 2; ++s) vt[s] = Ops::template column_slice<TileV>(tv, wave, lane, s);
+      const float G_first = lane_value(G, first);
+      const float d = static_cast<int>(li) == first ? 0.0f : G - G_first;
+      uint32_t ends = static_cast<uint32_t>(__ballot(!(fabsf(d) <= kMild))) | resets;
+      ResMax2 top;  // of the lane's column of v, steps 16 s + 8 half + e
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f32x4 t = *reinterpret_cast<const f32x4*>(&gates[wave][1][8 * i + 4 * half]);
-      wj[4 * i] = t.x, wj[4 * i + 1] = t.y, wj[4 * i + 2] = t.z, wj[4 * i + 3] = t.w;
-    }
-    frag vt[2];
+      for (int s = 0; s < 2; ++s) {
+        const f32x8 v = Ops::widen(vt[s]);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) vt[s] = Ops::template column_slice<RBV>(tv, wave * 32, lane, s);
-
-    if constexpr (kFull) {
-      const float e_i = since >= 0 ? 0.0f : __builtin_amdgcn_exp2f(G);
-      f32x16 P, O;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) P[r] = 0.0f, O[r] = 0.0f;
-      // scores k_j . q_i and what the state adds, S^T q_i
-#pragma unroll
-      for (int s = 0; s < 2 * KB; ++s) {
-        const frag q = Ops::template row_slice<RBK>(tq, li, half, s);
-        const frag k = Ops::template row_slice<RBK>(tk, li, half, s);
-        P = Ops::mma(k, q, P);
-        f32x8 sv;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sv[e] = S[s >> 1][8 * (s & 1) + e];
-        frag sf[NS];
-        Ops::template split<NS>(sv, sf);
-#pragma unroll
-        for (int n = NS - 1; n >= 0; --n) O = Ops::mma(sf[n], q, O);
+        for (int e = 0; e < 8; e += 2) res_max2(top, v[e], v[e + 1]);
       }
+      const bool odd = __ballot(!(top.v < kTame)) != 0;
+      uint32_t odds = 0;
+      if (odd) {
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+          const f32x8 v = Ops::widen(s == 0 ? vt[0] : vt[1]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 t = *reinterpret_cast<const f32x4*>(&gates[wave][0][8 * i + 4 * half]);
+          for (int e = 0; e < 8; ++e) {
+            const unsigned long long m = __ballot(!(fabsf(v[e]) < kTame));
+            if (static_cast<uint32_t>(m) != 0) odds |= 1u << (16 * s + e);
+            if ((m >> 32) != 0) odds |= 1u << (16 * s + 8 + e);
+          }
+        }
+        ends |= odds;
+      }
+      ends &= 0xfffffffeu << first;
+      const int last = ends != 0 ? __builtin_ctz(ends) : 32;  // one past the run
+      const uint32_t run = (0xffffffffu << first) & (0xffffffffu >> (32 - last));
+      // the decay into the run's first step; the state is scaled when its exponent needs it
+      const float g_first = lane_value(g2, first);
+      const bool drop = ((resets >> first) & 1u) != 0;
+      E += g_first;
+      if (drop || !(fabsf(E) <= kMild) || ((odds >> first) & 1u) != 0) {
+        const float f = __builtin_amdgcn_exp2f(E);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 8 * i + 4 * static_cast<int>(half) + e;
-          const bool in = j <= static_cast<int>(li) && j >= since;
-          const float d = __builtin_amdgcn_exp2f(G - t[e]) * R.v_scale;
-          P[4 * i + e] = in ? P[4 * i + e] * d : 0.0f;
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) S[kb][r] = drop ? 0.0f : S[kb][r] * f;
+        E = 0.0f;
+      }
+      if (odd) {  // what is not finite must not meet a factor of zero
+#pragma unroll
+        for (int s = 0; s < 2; ++s) vt[s] = Ops::keep(vt[s], run >> (16 * s + 8 * half));
+      }
+      const float x = E + d;
+      const bool in_run = ((run >> li) & 1u) != 0;
+      const float scale = __builtin_amdgcn_exp2f(-x) * v_scale;
+      if (lane < 32) scales[wave][lane] = in_run ? scale : 0.0f;
+      __builtin_amdgcn_wave_barrier();
+
+      f32x16 P, O;
+      if constexpr (kFull) {
+        // scores k_j . q_i, and what the state adds, S^T q_i
+#pragma unroll
+        for (int r = 0; r < 16; ++r) P[r] = 0.0f, O[r] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kSlices; ++s) {
+          const frag q = Ops::template row_slice<TileK>(tq, li, half, s);
+          const frag k = Ops::template row_slice<TileK>(tk, lin_swap(li), half, s);
+          frag sf[NS];
+          P = Ops::mma(k, q, P);
+          f32x8 sv;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sv[e] = S[s >> 1][8 * (s & 1) + e];
+          Ops::template split<NS>(sv, sf);
+#pragma unroll
+          for (int n = NS - 1; n >= 0; --n) O = Ops::mma(sf[n], q, O);
         }
       }
+      // v'_j = 2^-(E + G_j) v_s v_j of the run's steps
+      frag vw[2][NV];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) O[r] *= e_i;
-      if (__ballot(Ops::not_finite(vt[0]) || Ops::not_finite(vt[1])) == 0) {
+      for (int s = 0; s < 2; ++s) {
+        f32x8 v = Ops::widen(vt[s]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const f32x4 t = *reinterpret_cast<const f32x4*>(&scales[wave][16 * s + 8 * half + 4 * i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * i + e] *= t[e];
+        }
+        Ops::template split<NV>(v, vw[s]);
+      }
+      // ---- the state after the run, and + sum_{j <= i} (q_i . k_j) v'_j: the first half of the
+      // state's products runs while the scores are rounded, the second while those of the outputs end
+      auto state_products = [&](int from, int to) {
+#pragma unroll
+        for (int s = from; s < to; ++s) {
+          frag kt = Ops::template column_slice<TileK>(tk, s >> 1, lane, s & 1);
+          if (last - first != 32) {  // other steps' k are cleared, whatever they hold
+            asm volatile("");        // (a branch, not masks for every chunk)
+            kt = Ops::keep(kt, run >> (16 * (s & 1) + 8 * half));
+          }
+#pragma unroll
+          for (int n = NV - 1; n >= 0; --n) S[s >> 1] = Ops::mma(kt, vw[s & 1][n], S[s >> 1]);
+        }
+      };
+      if constexpr (kFull) {
+        frag pf[2][NP];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           f32x8 pv;
 #pragma unroll
           for (int e = 0; e < 8; ++e) pv[e] = P[8 * s + e];
-          frag pf[NP];
-          Ops::template split<NP>(pv, pf);
+          Ops::template split<NP>(pv, pf[s]);
+          // other steps' scores are cleared (they may be infinite)
 #pragma unroll
-          for (int n = NP - 1; n >= 0; --n) O = Ops::mma(vt[s], pf[n], O);
+          for (int m = 0; m < NP; ++m) pf[s][m] = Ops::apply(pf[s][m], earlier[s]);
         }
+        if (last - first != 32) {
+          asm volatile("");
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int m = 0; m < NP; ++m) pf[s][m] = Ops::keep(pf[s][m], run >> (16 * s + 8 * half));
+        }
+        state_products(0, kSlices / 2);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          // products of terms, down to the last kept one of either
+#pragma unroll
+          for (int n = NV - 1; n >= 0; --n)
+#pragma unroll
+            for (int m = NP - 1; m >= 0; --m)
+              if (n + m < (NV > NP ? NV : NP)) O = Ops::mma(vw[s][n], pf[s][m], O);
+        }
+        state_products(kSlices / 2, kSlices);
       } else {
-// row by row, the accumulators of P passing through its first one
-#pragma unroll 1
-        for (int r = 0; r < 16; ++r) {
-          const float mine = P[0], other = __shfl_xor(P[0], 32, 64);
-#pragma unroll 1
-          for (int hh = 0; hh < 2; ++hh) {
-            const int j = 8 * (r >> 2) + 4 * hh + (r & 3);
-            const float p = static_cast<int>(half) == hh ? mine : other;
-            if (j <= static_cast<int>(li) && j >= since) {
+        state_products(0, kSlices);
+      }
+      if constexpr (kFull) {
+        const float e_i = __builtin_amdgcn_exp2f(x) * o_scale;
 #pragma unroll
-              for (int c = 0; c < 16; ++c)
-                O[c] = fmaf(p, Ops::element(tv, RBV, lin_swizzle<RBV>(j), j, wave * 32 + 8 * (c >> 2) + 4 * half + (c & 3)), O[c]);
-            }
+        for (int r = 0; r < 16; ++r) O[r] *= e_i;
+        const bool in = in_run && p0 + static_cast<int>(li) < p_end;
+        const rsrc_t ro = lin_rsrc(base_o);
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          f32x8 o;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = O[8 * i + e];
+          if constexpr (kDots) {
+            const f32x8 t = Ops::unpack8(dot_in[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot = fmaf(t[e], o[e], dot);
           }
-#pragma unroll
-          for (int e = 0; e + 1 < 16; ++e) P[e] = P[e + 1];
+          Ops::store8(Ops::pack8(o), ro, in ? off_o[i] : kLinOutside);
+        }
+        if constexpr (kDots) {
+          dot += __shfl_xor(dot, 32, 64);
+          if (lane < 32 && in_run) dots[(p0 >> 5) & 1][wave][lane] = dot;
         }
       }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) O[r] *= R.o_scale;
-      if (R.dot_out != nullptr) {
-        const rsrc_t r = lin_rsrc(static_cast<const char*>(R.dot.data) +
-                                  (it.row * R.dot.sb + it.start * R.dot.st + it.head * R.dot.sh + static_cast<i64>(low_step(p0)) * R.dot.st) * kSize);
-        const bool in = p0 + static_cast<int>(li) < p_end;
-        const uint32_t row_off = static_cast<uint32_t>(row_step(p0, static_cast<int>(li))) * static_cast<uint32_t>(R.dot.st * kSize);
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = wave * 32 + 8 * i + 4 * static_cast<int>(half);
-          const f32x4 t = Ops::load4(r, in && c < VD ? row_off + c * kSize : kLinOutside);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s = fmaf(t[e], O[4 * i + e], s);
-        }
-        s += __shfl_xor(s, 32, 64);
-        if (lane < 32) dots[(p0 >> 5) & 1][wave][lane] = s;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) held[i] = Ops::pack4(O[4 * i], O[4 * i + 1], O[4 * i + 2], O[4 * i + 3]);
-    }
-
-    // ---- the state after the chunk ----
-    frag vw[2][NV];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      f32x8 v = Ops::widen(vt[s]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= wj[8 * s + e];
-      Ops::template split<NV>(v, vw[s]);
-    }
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) S[kb][r] *= decay;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const frag kt = Ops::template column_slice<RBK>(tk, kb * 32, lane, s);
-#pragma unroll
-        for (int n = NV - 1; n >= 0; --n) S[kb] = Ops::mma(kt, vw[s][n], S[kb]);
-      }
-    }
-    seg_decay *= decay;
+      const float d_last = lane_value(d, last - 1);
+      E += d_last;
+      seg_decay = drop ? 0.0f : seg_decay * __builtin_amdgcn_exp2f(g_first + d_last);
+      first = last;
+    } while (first < 32);
+    if constexpr (kFull) base_o += turn_o;
   };
 
   // ---- the walk: the loads of chunk c + 1 are in flight while chunk c is computed ----
-  float g_next = load_gate(p_begin + static_cast<int>(li));
-  auto step = [&](int c, unsigned char* cur, unsigned char* refill) {
+  // Memory operations complete in order: after the loads that a chunk waits for come the stores of
+  // the chunk before it, kStores at least, which may stay in flight.
+  constexpr int kStores = kFull ? (BF16 ? 2 : 4) : 0;
+  float g_next = load_gate(p_begin);
+  if (n_chunks > 0) issue(st0, p_end - p_begin);
+  auto step = [&](int c, lds_bytes cur, lds_bytes refill) {
     const int p0 = p_begin + 32 * c;
-    const float g = g_next;
-    lin_wait_loads();
+    if (kStages > 1 && c > 0) lin_wait_loads<kStores>();
+    else lin_wait_loads<0>();
     lin_barrier();
-    if (kFull && c > 0) store_held(p0 - 32);
-    if (c + 1 < n_chunks) {
-      g_next = load_gate(p0 + 32 + static_cast<int>(li));
-      if constexpr (kTwo) issue(refill, p0 + 32);
+    const float g = g_next;
+    if constexpr (kDots) {
+      if (c > 0) store_dots(p0 - 32);
+      load_dots(p0);
+    }
+    g_next = load_gate(p0 + 32);
+    if constexpr (kStages > 1) {
+      if (c + 1 < n_chunks) issue(refill, p_end - p0 - 32);
     }
     chunk(cur, p0, g);
-    if constexpr (!kTwo) {
+    if constexpr (kStages == 1) {
       lin_barrier();
-      if (c + 1 < n_chunks) issue(cur, p0 + 32);
+      if (c + 1 < n_chunks) issue(cur, p_end - p0 - 32);
     }
   };
-  if (n_chunks > 0) issue(st0, p_begin);
-  if constexpr (kTwo) {
-    int c = 0;
-    for (; c + 2 <= n_chunks; c += 2) {
+  for (int c = 0; c < n_chunks; ++c) {
+    if constexpr (kStages == 1) {
+      step(c, st0, st0);
+    } else {
       step(c, st0, st1);
-      step(c + 1, st1, st0);
+      if (++c == n_chunks) break;
+      step(c, st1, st0);
     }
-    if (c < n_chunks) step(c, st0, st1);
-  } else {
-    for (int c = 0; c < n_chunks; ++c) step(c, st0, st0);
   }
-  if (kFull && n_chunks > 0) {
+  if (kDots && n_chunks > 0) {
     lin_barrier();  // the waves' inner products of the last chunk
-    store_held(p_begin + 32 * (n_chunks - 1));
+    store_dots(p_begin + 32 * (n_chunks - 1));
   }
 
   // ---- the state the segment ends with ----
+  const float unit = __builtin_amdgcn_exp2f(E);
   if constexpr (!kFull) {
     float* to = R.seg_states + (static_cast<i64>(it.slot) * a.H + it.head) * KD * VD;
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int k = kb * 32 + 8 * (r >> 2) + 4 * static_cast<int>(half) + (r & 3);
-        if (k < KD && col < VD) to[k * VD + col] = S[kb][r];
+        const int k = kb * 32 + 16 * (r >> 3) + 8 * static_cast<int>(half) + (r & 7);
+        if (k < KD && col < VD) to[k * VD + col] = S[kb][r] * unit;
       }
     if (threadIdx.x == 0) R.seg_decays[static_cast<i64>(it.slot) * a.H + it.head] = seg_decay;
   } else if (p_end >= it.len) {
     // the gradient of the initial state also passes the first step's decay
-    float lead = 1.0f;
-    if (R.reverse && it.len > 0) lead = gate[0] <= kReset ? 0.0f : __builtin_amdgcn_exp2f(gate[0] * kLog2e);
+    float lead = unit;
+    if (R.reverse && it.len > 0) lead = gate[0] <= kReset ? 0.0f : unit * __builtin_amdgcn_exp2f(gate[0] * kLog2e);
     const i64 at = (static_cast<i64>(it.seq) * a.H + it.head) * KD * VD;
     if (R.state_out != nullptr) {
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int k = kb * 32 + 8 * (r >> 2) + 4 * static_cast<int>(half) + (r & 3);
+          const int k = kb * 32 + 16 * (r >> 3) + 8 * static_cast<int>(half) + (r & 7);
           if (k < KD && col < VD) R.state_out[at + k * VD + col] = S[kb][r] * lead;
         }
     }
@@ -594,10 +824,10 @@ __global__ __launch_bounds__(64 * VB, 2) void linear_walk_kernel(const LinLaunch
       for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int k = kb * 32 + 8 * (r >> 2) + 4 * static_cast<int>(half) + (r & 3);
+          const int k = kb * 32 + 16 * (r >> 3) + 8 * static_cast<int>(half) + (r & 7);
           if (k < KD && col < VD) s = fmaf(R.edge[at + static_cast<i64>(col) * KD + k], S[kb][r], s);
         }
-      s = wave_sum(s);
+      s = wave_sum(s) * unit;
       lin_barrier();
       if (lane == 0) dots[0][wave][0] = s;
       lin_barrier();
@@ -610,6 +840,34 @@ __global__ __launch_bounds__(64 * VB, 2) void linear_walk_kernel(const LinLaunch
   }
 }
 
+template <bool BF16, int KB, int VB, LinPass kPass>
+__global__ __launch_bounds__(64 * VB, 2) void linear_walk_kernel(const LinLaunch a) {
+  // workgroup -> (role, head, slot): the roles of an item follow each other on the same XCD
+  const int bid = blockIdx.x;
+  int role = 0, item = bid;
+  if (a.n_roles > 1) {
+    const int xcd = bid & 7, idx = bid >> 3;
+    role = idx % a.n_roles;
+    item = (idx / a.n_roles) * 8 + xcd;
+  }
+  if (item >= a.n_slots * a.H) return;
+  LinItem it;
+  if (!lin_item(a, item / a.H, item % a.H, it)) return;
+  const LinRole& R = a.role[role];
+  // bf16 terms: forward 1 for scores and state, whose outputs are bf16, and 2 for the scaled values,
+  // which the float32 state gathers; 3 (float32's 24 bits) where float32 inner products are wanted,
+  // whose sums cancel, and in a segment's state
+  constexpr int NV = BF16 ? 2 : 1, NX = BF16 ? 3 : 1;
+  if constexpr (kPass == LinPass::kStates) {
+    linear_walk<BF16, KB, VB, false, false, 1, 1, NX>(a, R, it);
+  } else if constexpr (kPass == LinPass::kForward) {
+    linear_walk<BF16, KB, VB, true, false, 1, 1, NV>(a, R, it);
+  } else {
+    if (R.dot_out != nullptr) linear_walk<BF16, KB, VB, true, true, NX, NX, NX>(a, R, it);
+    else linear_walk<BF16, KB, VB, true, false, 1, 1, NX>(a, R, it);
+  }
+}
+
 // ---- launches ------------------------------------------------------------------------------------
 template <bool BF16, int KB, int VB>
 hipError_t lin_launch(const LinLaunch& a, LinPass pass, hipStream_t st) {
@@ -617,12 +875,10 @@ hipError_t lin_launch(const LinLaunch& a, LinPass pass, hipStream_t st) {
   const long long blocks = a.n_roles == 1 ? items : (items + 7) / 8 * 8 * a.n_roles;
   if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks)), block(64 * VB);
-  constexpr int NF = BF16 ? 2 : 1;  // the forward: bf16 outputs, so one term for scores and state
-  constexpr int NB = BF16 ? 3 : 1;  // the float32 gradient of the decay: float32 precision throughout
   switch (pass) {
-    case LinPass::kStates: linear_walk_kernel<BF16, KB, VB, false, 1, 1, NB><<<grid, block, 0, st>>>(a); break;
-    case LinPass::kForward: linear_walk_kernel<BF16, KB, VB, true, 1, 1, NF><<<grid, block, 0, st>>>(a); break;
-    case LinPass::kExact: linear_walk_kernel<BF16, KB, VB, true, NB, NB, NB><<<grid, block, 0, st>>>(a); break;
+    case LinPass::kStates: linear_walk_kernel<BF16, KB, VB, LinPass::kStates><<<grid, block, 0, st>>>(a); break;
+    case LinPass::kForward: linear_walk_kernel<BF16, KB, VB, LinPass::kForward><<<grid, block, 0, st>>>(a); break;
+    case LinPass::kExact: linear_walk_kernel<BF16, KB, VB, LinPass::kExact><<<grid, block, 0, st>>>(a); break;
   }
   return hipGetLastError();
 }

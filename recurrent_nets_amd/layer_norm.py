@@ -16,10 +16,17 @@ def _rows(x, name):
     """(leading shape, rows, width) of a dense (..., width) tensor."""
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError(f"{name} must be (..., width) with width >= 1, got {tuple(x.shape)}")
-    rows = 1
-    for n in x.shape[:-1]:
-        rows *= n
-    return tuple(x.shape[:-1]), rows, x.shape[-1]
+    width = x.shape[-1]
+    return x.shape[:-1], x.numel() // width, width
+
+
+def _stat(t, name, lead, x, want):
+    """A given float32 output of shape `lead`, checked, or a new one if it is wanted."""
+    if t is None:
+        return x.new_empty(lead, dtype=torch.float32) if want else None
+    _dev(t, name, (torch.float32,))
+    _shape(t, name, lead)
+    return t
 
 
 def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None, mean=None, rstd=None,
@@ -31,22 +38,18 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=
     takes."""
     L = load()
     _dev(x, "x", _FLOATS)
-    _dev(weight, "weight", (torch.float32,))
-    _dev(bias, "bias", (torch.float32,))
     lead, rows, width = _rows(x, "x")
-    _shape(weight, "weight", (width,))
-    _shape(bias, "bias", (width,))
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _dev(t, name, (torch.float32,))
+            _shape(t, name, (width,))
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
-    _dev(out, "out", _FLOATS)
-    _shape(out, "out", x.shape)
-    if want_stats and mean is None:
-        mean = torch.empty(lead, dtype=torch.float32, device=x.device)
-    if want_stats and rstd is None:
-        rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _dev(t, name, (torch.float32,))
-        _shape(t, name, lead)
+        out = torch.empty_like(x, dtype=out_dtype)
+    else:
+        _dev(out, "out", _FLOATS)
+        _shape(out, "out", x.shape)
+    mean = _stat(mean, "mean", lead, x, want_stats)
+    rstd = _stat(rstd, "rstd", lead, x, want_stats)
     status = L.slstm_layer_norm_forward(_ptr(x), _dtype(x), _ptr(weight), _ptr(bias), float(eps), _ptr(out), _dtype(out),
                                         _ptr(mean), _ptr(rstd), rows, width, _stream(stream))
     _check(status, "slstm_layer_norm_forward")
@@ -74,15 +77,11 @@ def layer_norm_backward(x, g_y, mean, rstd, weight=None, dx=None, dweight=None, 
         _shape(t, name, lead)
     if dx is None:
         dx = torch.empty_like(x)
-    if want_dweight and dweight is None:
-        dweight = torch.empty(width, dtype=torch.float32, device=x.device)
-    if want_dbias and dbias is None:
-        dbias = torch.empty(width, dtype=torch.float32, device=x.device)
-    _dev(dx, "dx", (x.dtype,))
-    _shape(dx, "dx", x.shape)
-    for name, t in (("dweight", dweight), ("dbias", dbias)):
-        _dev(t, name, (torch.float32,))
-        _shape(t, name, (width,))
+    else:
+        _dev(dx, "dx", (x.dtype,))
+        _shape(dx, "dx", x.shape)
+    dweight = _stat(dweight, "dweight", (width,), x, want_dweight)
+    dbias = _stat(dbias, "dbias", (width,), x, want_dbias)
     if workspace is None and (dweight is not None or dbias is not None):
         workspace = alloc_workspace(L.slstm_layer_norm_backward_workspace_bytes(rows, width), x.device)
     status = L.slstm_layer_norm_backward(_ptr(x), _dtype(x), _ptr(g_y), _dtype(g_y), _ptr(mean), _ptr(rstd), _ptr(weight),

@@ -27,14 +27,14 @@ def _view(t, name, dtype, shape):
         raise ValueError(f"{name} must be a device tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1:
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
-    st = [0 if n <= 1 else s for n, s in zip(t.shape, t.stride())]
-    if len(shape) == 3:  # a single step: (B, H, width)
-        return _Heads(t.data_ptr(), st[0], 0, st[1])
-    return _Heads(t.data_ptr(), st[0], st[1], st[2])
+    sb = st[0] if shape[0] > 1 else 0
+    sh = st[-2] if shape[-2] > 1 else 0
+    return _Heads(t.data_ptr(), sb, st[1] if len(st) == 4 and shape[1] > 1 else 0, sh)
 
 
 def _own(t, name):
@@ -43,22 +43,23 @@ def _own(t, name):
         raise ValueError(f"{name} must not share elements (a stride of 0)")
 
 
-def _shapes(q, v, steps=True):
-    n = 4 if steps else 3
-    what = "(B, T, n_heads, d)" if steps else "(B, n_heads, d)"
-    for name, t in (("q", q), ("v", v)):
-        if t.dim() != n:
-            raise ValueError(f"{name} must be {what}, got {tuple(t.shape)}")
+def _shapes(q, v, dims, what):
+    """(q's shape, v's), of `dims` axes."""
+    if q.dim() != dims or v.dim() != dims:
+        raise ValueError(f"q and v must be {what}, got {tuple(q.shape)}, {tuple(v.shape)}")
     if q.dtype not in _FLOATS:
         raise TypeError(f"q must be one of {_FLOATS}, got {q.dtype}")
-    return tuple(q.shape), tuple(v.shape[:-1]) + (v.shape[-1],)
+    return q.shape, q.shape[:-1] + v.shape[-1:]
+
+
+_STEPS, _ONE = (4, "(B, T, n_heads, d)"), (3, "(B, n_heads, d)")
 
 
 def _decay(log_decay, lead):
     """Whether log_decay is one value per head (n_heads) rather than per step and head."""
     _dev(log_decay, "log_decay", (torch.float32,))
     per_head = log_decay.dim() == 1
-    _shape(log_decay, "log_decay", (lead[-1],) if per_head else lead)
+    _shape(log_decay, "log_decay", lead[-1:] if per_head else lead)
     return int(per_head)
 
 
@@ -87,16 +88,16 @@ def linear_attention_forward(q, k, v, log_decay, state0=None, scale=None, out=No
     ``cu_seqlens`` (S + 1 offsets) packs S sequences end to end in one row, as in newton_forward:
     the states are then (S, n_heads, d_key, d_value)."""
     L = load()
-    shape, vshape = _shapes(q, v)
+    shape, vshape = _shapes(q, v, *_STEPS)
     B, T, H, dk = shape
     dv = vshape[-1]
     cu, S = _seqs(cu_seqlens, q)
-    views = [_view(q, "q", q.dtype, shape), _view(k, "k", q.dtype, shape), _view(v, "v", q.dtype, (B, T, H, dv))]
-    per_head = _decay(log_decay, (B, T, H))
+    views = [_view(q, "q", q.dtype, shape), _view(k, "k", q.dtype, shape), _view(v, "v", q.dtype, vshape)]
+    per_head = _decay(log_decay, shape[:-1])
     n = B if cu is None else S
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
-    o = _view(out, "out", q.dtype, (B, T, H, dv))
+        out = q.new_empty(vshape)
+    o = _view(out, "out", q.dtype, vshape)
     _own(out, "out")
     if want_final_state and final_state is None:
         final_state = torch.empty((n, H, dk, dv), dtype=torch.float32, device=q.device)
@@ -122,20 +123,22 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None, out
     names each row's state (a slot outside the pool: the row is skipped, its output zero; no slot
     twice), without it row b has state b."""
     L = load()
-    shape, vshape = _shapes(q, v, steps=False)
+    shape, vshape = _shapes(q, v, *_ONE)
     B, H, dk = shape
     dv = vshape[-1]
-    views = [_view(q, "q", q.dtype, shape), _view(k, "k", q.dtype, shape), _view(v, "v", q.dtype, (B, H, dv))]
-    per_head = _decay(log_decay, (B, H))
+    views = [_view(q, "q", q.dtype, shape), _view(k, "k", q.dtype, shape), _view(v, "v", q.dtype, vshape)]
+    per_head = _decay(log_decay, shape[:-1])
     _dev(state, "state", (torch.float32,))
-    if state.dim() != 4 or tuple(state.shape[1:]) != (H, dk, dv):
+    if state.dim() != 4 or state.shape[1:] != (H, dk, dv):
         raise ValueError(f"state must be (n_slots, {H}, {dk}, {dv}), got {tuple(state.shape)}")
-    _dev(slots, "slots", (torch.int32,))
-    _shape(slots, "slots", (B,))
+    if slots is not None:
+        _dev(slots, "slots", (torch.int32,))
+        _shape(slots, "slots", (B,))
     if out is None:
-        out = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
-    _dev(out, "out", (q.dtype,))
-    _shape(out, "out", (B, H, dv))
+        out = q.new_empty(vshape)
+    else:
+        _dev(out, "out", (q.dtype,))
+        _shape(out, "out", vshape)
     status = L.slstm_linear_attention_step(*map(_ref, views), BF16 if q.dtype == torch.bfloat16 else F32,
                                            _ptr(log_decay), per_head, _ptr(state), _ptr(slots), state.shape[0],
                                            _scale(scale, dk), _ptr(out), B, H, dk, dv, _stream(stream))
@@ -157,13 +160,12 @@ def linear_attention_backward(q, k, v, log_decay, g_out, state0=None, g_final=No
     views (slices of one (B, T, 4, d_h) gradient); dlog_decay (B, T, n_heads) float32 is formed
     unless ``want_dlog_decay`` is False or the decay is fixed per head."""
     L = load()
-    shape, vshape = _shapes(q, v)
+    shape, vshape = _shapes(q, v, *_STEPS)
     B, T, H, d_key = shape
     d_value = vshape[-1]
-    vshape = (B, T, H, d_value)
     cu, S = _seqs(cu_seqlens, q)
     dt = q.dtype
-    per_head = _decay(log_decay, (B, T, H))
+    per_head = _decay(log_decay, shape[:-1])
     views = [_view(q, "q", dt, shape), _view(k, "k", dt, shape), _view(v, "v", dt, vshape)]
     g = _view(g_out, "g_out", dt, vshape)
     if want_dlog_decay is None:
@@ -177,7 +179,7 @@ def linear_attention_backward(q, k, v, log_decay, g_out, state0=None, g_final=No
         _dev(t, name, (torch.float32,))
         _shape(t, name, (n, H, d_key, d_value))
     _dev(dlog_decay, "dlog_decay", (torch.float32,))
-    _shape(dlog_decay, "dlog_decay", (B, T, H))
+    _shape(dlog_decay, "dlog_decay", shape[:-1])
     dq, dk, dv = (torch.empty(s, dtype=dt, device=q.device) if t is None else t
                   for t, s in ((dq, shape), (dk, shape), (dv, vshape)))
     outs = [_view(t, name, dt, s) for name, t, s in (("dq", dq, shape), ("dk", dk, shape), ("dv", dv, vshape))]
