@@ -138,13 +138,15 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const LinLaunch a) {
 // ---- the gradient of the log decays ------------------------------------------------------------------
 // dL/dg_t = <L_t, e^{g_t} S_{t-1}>, for which dg_t - dg_{t+1} = q_t . dq_t - k_t . dk_t: a sum from
 // the end, begun with <gradient of the final state, final state>. One workgroup a (sequence, head),
-// 1024 steps at a time from the end. The sums run in 64 bits: their terms cancel over the whole
+// 4096 steps at a time from the end. The sums run in 64 bits: their terms cancel over the whole
 // sequence while dg stays of the size that the decays remember. Bytes are those of three floats a
 // step, a few per cent of the operands'.
-__global__ __launch_bounds__(256) void linear_gate_gradient_kernel(const float* __restrict__ r, const float* __restrict__ c,
+constexpr int kGateThreads = 1024;
+
+__global__ __launch_bounds__(kGateThreads) void linear_gate_gradient_kernel(const float* __restrict__ r, const float* __restrict__ c,
                                                                    const float* __restrict__ edge, const LinLaunch a,
                                                                    float* __restrict__ dgate) {
-  __shared__ double waves[4];
+  __shared__ double waves[kGateThreads / 64];
   const int seq = blockIdx.x / a.H, head = blockIdx.x % a.H;
   int start = 0, len = a.T;
   i64 row = seq;
@@ -158,7 +160,7 @@ __global__ __launch_bounds__(256) void linear_gate_gradient_kernel(const float* 
   float* out = dgate + (row * static_cast<i64>(a.T) + start) * a.H + head;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   double carry = edge != nullptr ? static_cast<double>(edge[blockIdx.x]) : 0.0;
-  for (int end = len; end > 0; end -= 1024) {
+  for (int end = len; end > 0; end -= 4 * kGateThreads) {
     // thread i holds steps end - 1 - 4 i .. end - 4 - 4 i, latest first
     double s[4], total = 0.0;
 #pragma unroll
@@ -177,7 +179,7 @@ __global__ __launch_bounds__(256) void linear_gate_gradient_kernel(const float* 
     __syncthreads();
     double before = carry + (inc - total);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < kGateThreads / 64; ++w) {
       if (w < wave) before += waves[w];
       carry += waves[w];
     }
@@ -249,7 +251,7 @@ hipError_t launch_linear_join(const LinLaunch& a, hipStream_t st) {
 
 hipError_t launch_linear_gate_gradient(const float* r, const float* c, const float* edge, const LinLaunch& a,
                                        float* dgate, hipStream_t st) {
-  linear_gate_gradient_kernel<<<static_cast<unsigned>(a.n_seqs) * a.H, 256, 0, st>>>(r, c, edge, a, dgate);
+  linear_gate_gradient_kernel<<<static_cast<unsigned>(a.n_seqs) * a.H, kGateThreads, 0, st>>>(r, c, edge, a, dgate);
   return hipGetLastError();
 }
 
