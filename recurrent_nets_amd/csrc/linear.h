@@ -151,10 +151,51 @@ __device__ __forceinline__ float lin_clear(float v, uint32_t bits, int i) {
 template <bool BF16>
 struct LinOps;
 
+// The first N bf16 terms of 8 values, each the rounding of what the ones before it leave. What is
+// left of a pair's values is formed by the two-term dot product with (-1, 0) and (0, -1), exact as a
+// difference of nearby numbers: one instruction a value, where widening first would take two.
+template <int N>
+__device__ __forceinline__ void lin_terms(f32x8 v, bf16x8 (&out)[N]) {
+  union { uint32_t u; bf16x2 b; } first, second;
+  // kept in registers: as constants the compiler would encode them as operands of another type
+  if constexpr (N > 1) {
+    asm("v_mov_b32 %0, 0xbf80" : "=v"(first.u));
+    asm("v_mov_b32 %0, 0xbf800000" : "=v"(second.u));
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    out[n] = __builtin_convertvector(v, bf16x8);
+    if (n + 1 < N) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bf16x2 pair = {out[n][2 * i], out[n][2 * i + 1]};
+        v[2 * i] = __builtin_amdgcn_fdot2_f32_bf16(pair, first.b, v[2 * i], false);
+        v[2 * i + 1] = __builtin_amdgcn_fdot2_f32_bf16(pair, second.b, v[2 * i + 1], false);
+      }
+    }
+  }
+}
+
+// the elements of 8 bf16 values whose bits are set, as a mask to be made once, and its use
+__device__ __forceinline__ u32x4 lin_mask(uint32_t bits) {
+  u32x4 m;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = (lin_all(bits, 2 * i) & 0xffffu) | (lin_all(bits, 2 * i + 1) << 16);
+  return m;
+}
+__device__ __forceinline__ bf16x8 lin_masked(bf16x8 f, u32x4 m) {
+  union { bf16x8 f; u32x4 u; } r{f};
+  r.u &= m;
+  return r.f;
+}
+
+// `raw`: 8 values as they are stored; `frag`: an operand of a product
 template <>
 struct LinOps<true> {
+  typedef bf16x8 raw;
   typedef bf16x8 frag;
   static constexpr int kSize = 2;
+  static __device__ __forceinline__ frag operand(raw r) { return r; }
 
   static __device__ __forceinline__ f32x16 mma(const frag& a, const frag& b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -195,45 +236,10 @@ struct LinOps<true> {
     return v;
   }
   // the elements whose bits are set, zeros elsewhere
-  static __device__ __forceinline__ frag keep(frag f, uint32_t bits) {
-    return apply(f, mask_of(bits));
-  }
-  // v as N bf16 terms, each the rounding of what the ones before it leave. What is left of a pair's
-  // values is formed by the two-term dot product with (-1, 0) and (0, -1), exact as a difference of
-  // nearby numbers: one instruction a value, where widening first would take two.
+  static __device__ __forceinline__ raw keep(raw f, uint32_t bits) { return lin_masked(f, lin_mask(bits)); }
   template <int N>
   static __device__ __forceinline__ void split(f32x8 v, frag (&out)[N]) {
-    union { uint32_t u; bf16x2 b; } first, second;
-    // kept in registers: as constants the compiler would encode them as operands of another type
-    if constexpr (N > 1) {
-      asm("v_mov_b32 %0, 0xbf80" : "=v"(first.u));
-      asm("v_mov_b32 %0, 0xbf800000" : "=v"(second.u));
-    }
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      out[n] = __builtin_convertvector(v, frag);
-      if (n + 1 < N) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bf16x2 pair = {out[n][2 * i], out[n][2 * i + 1]};
-          v[2 * i] = __builtin_amdgcn_fdot2_f32_bf16(pair, first.b, v[2 * i], false);
-          v[2 * i + 1] = __builtin_amdgcn_fdot2_f32_bf16(pair, second.b, v[2 * i + 1], false);
-        }
-      }
-    }
-  }
-  // keep() as a mask made once
-  typedef u32x4 mask;
-  static __device__ __forceinline__ mask mask_of(uint32_t bits) {
-    mask m;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m[i] = (lin_all(bits, 2 * i) & 0xffffu) | (lin_all(bits, 2 * i + 1) << 16);
-    return m;
-  }
-  static __device__ __forceinline__ frag apply(frag f, mask m) {
-    union { frag f; u32x4 u; } r{f};
-    r.u &= m;
-    return r.f;
+    lin_terms<N>(v, out);
   }
   // 8 values of a row of global memory at a byte offset, and back
   typedef frag packed8;
@@ -249,50 +255,59 @@ struct LinOps<true> {
   }
 };
 
+// float32 values as three bf16 terms (24 bits) and products of the six pairs of terms above 2^-24 of
+// the whole: 6 products of 32 cycles for each 16 of the contraction index, where the float32 matrix
+// instructions take 8 of 64 (training on float32, 8 x 1024 steps, 4 heads of 64: 88 us, against 104
+// with those).
 template <>
 struct LinOps<false> {
-  typedef f32x8 frag;
+  typedef f32x8 raw;
+  struct frag {
+    bf16x8 t[3];
+  };
   static constexpr int kSize = 4;
-
+  static __device__ __forceinline__ frag operand(raw v) {
+    frag f;
+    lin_terms<3>(v, f.t);
+    return f;
+  }
   static __device__ __forceinline__ f32x16 mma(const frag& a, const frag& b, f32x16 c) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+    for (int n = 2; n >= 0; --n)
+#pragma unroll
+      for (int m = 0; m <= n; ++m) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.t[m], b.t[n - m], c, 0, 0, 0);
     return c;
   }
   template <class Tile>
-  static __device__ __forceinline__ frag row_slice(lds_bytes tile, uint32_t row, uint32_t half, int s) {
+  static __device__ __forceinline__ raw row_slice(lds_bytes tile, uint32_t row, uint32_t half, int s) {
     const uint32_t base = row * Tile::kLine + ((Tile::permute(row) ^ (2u * half)) << 4);
     const lds_bytes group = tile + (s >> 1) * Tile::kGroup;
-    union { f32x4 v[2]; frag f; } r;
+    union { f32x4 v[2]; raw f; } r;
     r.v[0] = lds_load<f32x4>(group + (base ^ static_cast<uint32_t>((s & 1) << 6)));
     r.v[1] = lds_load<f32x4>(group + (base ^ static_cast<uint32_t>((s & 1) << 6 | 16)));
     return r.f;
   }
   template <class Tile>
-  static __device__ __forceinline__ frag column_slice(lds_bytes tile, int block, uint32_t lane, int s) {
+  static __device__ __forceinline__ raw column_slice(lds_bytes tile, int block, uint32_t lane, int s) {
     const uint32_t row = 8u * (lane >> 5), col = lin_swap(lane & 31u);
     const uint32_t base = row * Tile::kLine + (((col >> 2) ^ Tile::permute(row)) << 4) + 4u * (col & 3u);
     const lds_bytes group = tile + block * Tile::kGroup + s * 16 * Tile::kLine;
-    frag f;
+    raw f;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       f[e] = lds_load<float>(group + e * Tile::kLine + (base ^ static_cast<uint32_t>((e & 2) << 5 | (e & 4) << 3)));
     return f;
   }
-  static __device__ __forceinline__ f32x8 widen(const frag& f) { return f; }
-  // keep() as a mask made once
-  typedef uint32_t mask;
-  static __device__ __forceinline__ mask mask_of(uint32_t bits) { return bits; }
-  static __device__ __forceinline__ frag apply(frag f, mask m) { return keep(f, m); }
-  static __device__ __forceinline__ frag keep(frag f, uint32_t bits) {
+  static __device__ __forceinline__ f32x8 widen(const raw& f) { return f; }
+  static __device__ __forceinline__ raw keep(raw f, uint32_t bits) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = lin_clear(f[e], bits, e);
     return f;
   }
   template <int N>
   static __device__ __forceinline__ void split(f32x8 v, frag (&out)[N]) {
-    static_assert(N == 1, "float32 operands are not split");
-    out[0] = v;
+    static_assert(N == 1, "float32 operands hold their terms");
+    out[0] = operand(v);
   }
   static __device__ __forceinline__ f32x8 load8(rsrc_t r, uint32_t off) {
     union { u32x4 u[2]; f32x8 f; } v;
@@ -362,7 +377,8 @@ struct lin_type {
 // LDS of a workgroup: the tiles, the steps' factors of v (a copy a wave) and the waves' parts of inner
 // products. Two stages (as two objects: the compiler then sees which one is being filled) where 8
 // waves still fit a compute unit; a second wave on a SIMD is worth more than loads a chunk ahead
-// (float32 training, 8 x 1024 steps, 4 heads of 64: see the stages' figures below).
+// (float32 training, 8 x 1024 steps, 4 heads of 64: 105 us, against 110 with two stages and half of
+// the waves).
 template <bool BF16, int KB, int VB, bool kFull>
 struct LinShape {
   typedef LinOps<BF16> Ops;
@@ -578,9 +594,9 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
   // first one leave 2^+-kMild, before a reset and before a step with values of kTame or more (or not
   // finite: those then reach no earlier row); what remains is taken as further runs.
   constexpr int kSlices = 2 * KB;
-  typename Ops::mask earlier[2];  // of the scores of step i = li: steps j <= i
+  u32x4 earlier[2];  // of the scores of step i = li: steps j <= i
 #pragma unroll
-  for (int s = 0; s < 2; ++s) earlier[s] = Ops::mask_of((0xffffffffu >> (31u - li)) >> (16 * s + 8 * half));
+  for (int s = 0; s < 2; ++s) earlier[s] = lin_mask((0xffffffffu >> (31u - li)) >> (16 * s + 8 * half));
   auto chunk = [&](lds_bytes stg, int p0, float g) {
     const lds_bytes tk = stg;
     const lds_bytes tv = stg + kTileK;
@@ -590,7 +606,7 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
     const float G = lin_scan32(g2);
     int first = 0;
     do {
-      frag vt[2];
+      typename Ops::raw vt[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) vt[s] = Ops::template column_slice<TileV>(tv, wave, lane, s);
       const float G_first = lane_value(G, first);
@@ -650,8 +666,8 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
         for (int r = 0; r < 16; ++r) P[r] = 0.0f, O[r] = 0.0f;
 #pragma unroll
         for (int s = 0; s < kSlices; ++s) {
-          const frag q = Ops::template row_slice<TileK>(tq, li, half, s);
-          const frag k = Ops::template row_slice<TileK>(tk, lin_swap(li), half, s);
+          const frag q = Ops::operand(Ops::template row_slice<TileK>(tq, li, half, s));
+          const frag k = Ops::operand(Ops::template row_slice<TileK>(tk, lin_swap(li), half, s));
           frag sf[NS];
           P = Ops::mma(k, q, P);
           f32x8 sv;
@@ -677,36 +693,47 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
       }
       // ---- the state after the run, and + sum_{j <= i} (q_i . k_j) v'_j: the first half of the
       // state's products runs while the scores are rounded, the second while those of the outputs end
+      const bool part = last - first != 32;
       auto state_products = [&](int from, int to) {
 #pragma unroll
         for (int s = from; s < to; ++s) {
-          frag kt = Ops::template column_slice<TileK>(tk, s >> 1, lane, s & 1);
-          if (last - first != 32) {  // other steps' k are cleared, whatever they hold
-            asm volatile("");        // (a branch, not masks for every chunk)
-            kt = Ops::keep(kt, run >> (16 * (s & 1) + 8 * half));
+          typename Ops::raw raw_kt = Ops::template column_slice<TileK>(tk, s >> 1, lane, s & 1);
+          if (part) {  // other steps' k are cleared, whatever they hold
+            asm volatile("");  // (a branch, not masks for every chunk)
+            raw_kt = Ops::keep(raw_kt, run >> (16 * (s & 1) + 8 * half));
           }
+          const frag kt = Ops::operand(raw_kt);
 #pragma unroll
           for (int n = NV - 1; n >= 0; --n) S[s >> 1] = Ops::mma(kt, vw[s & 1][n], S[s >> 1]);
         }
       };
       if constexpr (kFull) {
+        // scores of the run's steps up to i; others may be infinite or NaN: one term is cleared as
+        // it is, several before they are formed, for a pair's values meet in them
         frag pf[2][NP];
+        if constexpr (BF16 && NP == 1) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          f32x8 pv;
+          for (int s = 0; s < 2; ++s) {
+            f32x8 pv;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) pv[e] = P[8 * s + e];
-          Ops::template split<NP>(pv, pf[s]);
-          // other steps' scores are cleared (they may be infinite)
+            for (int e = 0; e < 8; ++e) pv[e] = P[8 * s + e];
+            Ops::template split<NP>(pv, pf[s]);
+            pf[s][0] = lin_masked(pf[s][0], earlier[s]);
+          }
+          if (part) {
+            asm volatile("");
 #pragma unroll
-          for (int m = 0; m < NP; ++m) pf[s][m] = Ops::apply(pf[s][m], earlier[s]);
-        }
-        if (last - first != 32) {
-          asm volatile("");
+            for (int s = 0; s < 2; ++s) pf[s][0] = lin_masked(pf[s][0], lin_mask(run >> (16 * s + 8 * half)));
+          }
+        } else {
+          const uint32_t bits = (run & (0xffffffffu >> (31u - li))) >> (8 * half);
 #pragma unroll
-          for (int s = 0; s < 2; ++s)
+          for (int s = 0; s < 2; ++s) {
+            f32x8 pv;
 #pragma unroll
-            for (int m = 0; m < NP; ++m) pf[s][m] = Ops::keep(pf[s][m], run >> (16 * s + 8 * half));
+            for (int e = 0; e < 8; ++e) pv[e] = lin_clear(P[8 * s + e], bits, 16 * s + e);
+            Ops::template split<NP>(pv, pf[s]);
+          }
         }
         state_products(0, kSlices / 2);
 #pragma unroll

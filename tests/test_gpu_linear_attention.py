@@ -318,18 +318,32 @@ def test_what_is_not_finite_stays_in_the_future(amd, where, bad, dtype):
     assert not bool(o[:, at].isfinite().all()) and not bool(S.isfinite().all())
 
 
-@pytest.mark.parametrize("where,name", [("k", "dq"), ("q", "dk"), ("go", "dv")])
-def test_gradients_keep_to_their_side_too(amd, where, name):
-    """dq takes earlier keys; dk and dv take later queries and gradients."""
-    p = Problem(37, 1, 90, 1, 32, 32, "bf16")
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("where,name", [("k", "dq"), ("v", "dq"), ("q", "dk"), ("go", "dk"), ("go", "dv"), ("q", "dv")])
+def test_gradients_keep_to_their_side_too(amd, where, name, dtype):
+    """dq takes earlier keys and values; dk and dv take later queries and gradients."""
+    p = Problem(37, 1, 90, 1, 32, 32, dtype)
     clean = dict(zip(("dq", "dk", "dv"), amd.linear_attention_backward(p.q, p.k, p.v, p.g, p.go, p.s0, scale=p.scale)))
     getattr(p, where)[:, 45, :, 3] = float("nan")
-    case(f"linear attention gradients with NaN in {where}")
+    case(f"linear attention gradients with NaN in {where} {dtype}")
     got = dict(zip(("dq", "dk", "dv"), amd.linear_attention_backward(p.q, p.k, p.v, p.g, p.go, p.s0, scale=p.scale)))
     torch.cuda.synchronize()
     side = slice(0, 45) if name == "dq" else slice(46, 90)
     assert bool(got[name][:, side].isfinite().all())
-    assert _rel(got[name][:, side], to_np(clean[name][:, side])) < BF16_BAR
+    assert _rel(got[name][:, side], to_np(clean[name][:, side])) < p.bar
+
+
+def test_steps_after_a_reset_do_not_see_what_was_before(amd):
+    """Whatever it was: NaN in an earlier document stays there."""
+    p = Problem(39, 1, 100, 2, 32, 32, "bf16", gate=_starts)
+    clean, S = amd.linear_attention_forward(p.q, p.k, p.v, p.g, p.s0, scale=p.scale, want_final_state=True)
+    p.k[:, 50, :, 3] = float("nan")
+    p.v[:, 51, :, 3] = float("inf")
+    case("linear attention, NaN before a reset")
+    o, S2 = amd.linear_attention_forward(p.q, p.k, p.v, p.g, p.s0, scale=p.scale, want_final_state=True)
+    torch.cuda.synchronize()
+    assert torch.equal(o[:, 64:], clean[:, 64:]) and torch.equal(S, S2)
+    assert torch.equal(o[:, :50], clean[:, :50])
 
 
 # ---- single tokens --------------------------------------------------------------------------------
