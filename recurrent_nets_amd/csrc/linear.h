@@ -541,7 +541,11 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
       const int k = kb * 32 + 16 * (r >> 3) + 8 * static_cast<int>(half) + (r & 7);
       S[kb][r] = buf_ld(r_from, has && k < KD ? static_cast<uint32_t>(k * rs + col * cs) * 4u : kLinOutside, 0);
     }
-  float E = 0.0f;  // the state is 2^E S
+  double E = 0.0;  // the state is 2^E S; 64 bits, for a long memory adds many small decays
+  auto power = [](double e) {  // 2^e
+    const double n = __builtin_rint(e);
+    return __builtin_ldexpf(__builtin_amdgcn_exp2f(static_cast<float>(e - n)), static_cast<int>(n));
+  };
   float seg_decay = 1.0f;
 
   // outputs: a lane holds 2 runs of 8 columns of a step
@@ -640,22 +644,25 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
       // the decay into the run's first step; the state is scaled when its exponent needs it
       const float g_first = lane_value(g2, first);
       const bool drop = ((resets >> first) & 1u) != 0;
-      E += g_first;
-      if (drop || !(fabsf(E) <= kMild) || ((odds >> first) & 1u) != 0) {
-        const float f = __builtin_amdgcn_exp2f(E);
+      E += static_cast<double>(g_first);
+      if (drop || !(fabs(E) <= static_cast<double>(kMild)) || ((odds >> first) & 1u) != 0) {
+        const float f = power(E);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
           for (int r = 0; r < 16; ++r) S[kb][r] = drop ? 0.0f : S[kb][r] * f;
-        E = 0.0f;
+        E = 0.0;
       }
       if (odd) {  // what is not finite must not meet a factor of zero
 #pragma unroll
         for (int s = 0; s < 2; ++s) vt[s] = Ops::keep(vt[s], run >> (16 * s + 8 * half));
       }
-      const float x = E + d;
+      // 2^(E + d) and its inverse, the whole part of E apart so that its size costs d no digits
+      const double whole = __builtin_rint(E);
+      const int n_E = static_cast<int>(whole);
+      const float x = static_cast<float>(E - whole) + d;
       const bool in_run = ((run >> li) & 1u) != 0;
-      const float scale = __builtin_amdgcn_exp2f(-x) * v_scale;
+      const float scale = __builtin_ldexpf(__builtin_amdgcn_exp2f(-x), -n_E) * v_scale;
       if (lane < 32) scales[wave][lane] = in_run ? scale : 0.0f;
       __builtin_amdgcn_wave_barrier();
 
@@ -751,7 +758,7 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
         state_products(0, kSlices);
       }
       if constexpr (kFull) {
-        const float e_i = __builtin_amdgcn_exp2f(x) * o_scale;
+        const float e_i = __builtin_ldexpf(__builtin_amdgcn_exp2f(x), n_E) * o_scale;
 #pragma unroll
         for (int r = 0; r < 16; ++r) O[r] *= e_i;
         const bool in = in_run && p0 + static_cast<int>(li) < p_end;
@@ -775,7 +782,7 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
         }
       }
       const float d_last = lane_value(d, last - 1);
-      E += d_last;
+      E += static_cast<double>(d_last);
       seg_decay = drop ? 0.0f : seg_decay * __builtin_amdgcn_exp2f(g_first + d_last);
       first = last;
     } while (first < 32);
@@ -823,7 +830,7 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
   }
 
   // ---- the state the segment ends with ----
-  const float unit = __builtin_amdgcn_exp2f(E);
+  const float unit = power(E);
   if constexpr (!kFull) {
     float* to = R.seg_states + (static_cast<i64>(it.slot) * a.H + it.head) * KD * VD;
 #pragma unroll

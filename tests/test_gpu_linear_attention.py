@@ -225,6 +225,19 @@ def _growing(g, r):
     return r.uniform(-0.2, 0.1, g.shape)
 
 
+def _long(g, r):
+    return -10.0 ** r.uniform(-5, -2.5, g.shape[-1:]) * np.ones(g.shape)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_long_memories(amd, dtype):
+    """Decays that remember thousands of steps, over as many: small exponents add up exactly."""
+    p = Problem(16, 1, 3000, 6, 32, 32, dtype, gate=_long, g_final=True)
+    case(f"linear attention, long memories {dtype}")
+    p.check_forward(amd)
+    p.check_backward(amd)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("gate", [_starts, _all_resets, _no_decay, _strong, _growing])
 def test_decays(amd, gate, dtype):
