@@ -147,6 +147,15 @@ __device__ __forceinline__ float lin_clear(float v, uint32_t bits, int i) {
   return __uint_as_float(__float_as_uint(v) & lin_all(bits, i));
 }
 
+// A value that is the same in every lane, kept in scalar registers: the compiler would read launch
+// arguments again in every chunk, a memory round trip each.
+template <class T>
+__device__ __forceinline__ T lin_kept(T v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+__device__ __forceinline__ bool rarely(bool v) { return __builtin_expect(v, false); }
+
 // ---- operand slices: 8 values a lane, in the accumulators' row order --------------------------
 template <bool BF16>
 struct LinOps;
@@ -424,8 +433,8 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
   const int wave = VB == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t half = static_cast<uint32_t>(lane) >> 5, li = static_cast<uint32_t>(lane) & 31u;
   const int KD = R.KD, VD = R.VD;
-  // kept (as values of a lane), where the compiler would read the arguments again in every chunk
-  const float o_scale = lane_value(R.o_scale, 0), v_scale = lane_value(R.v_scale, 0);
+  const float o_scale = lin_kept(R.o_scale), v_scale = lin_kept(R.v_scale);
+  const int reverse = lin_kept(R.reverse);
   const int p_begin = it.seg * a.seg_len;
   const int p_end = min(it.len, p_begin + a.seg_len);
   const int n_chunks = max(0, (p_end - p_begin + 31) >> 5);
@@ -434,13 +443,13 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
   // Tiles are addressed from the lowest step of their chunk: forward in time the step of the row 0,
   // backward that of row 31, which in a sequence's last chunk may lie before its first step (rows
   // past the end are never fetched). The address moves by 32 steps a chunk, a lane's offsets stay.
-  const int low = R.reverse ? it.len - 32 - p_begin : p_begin;
-  const int turn = R.reverse ? -32 : 32;
+  const int low = reverse ? it.len - 32 - p_begin : p_begin;
+  const int turn = reverse ? -32 : 32;
   auto at_first = [&](const LinView& v) {
     return static_cast<const char*>(v.data) +
            (it.row * v.sb + (static_cast<i64>(it.start) + low) * v.st + it.head * v.sh) * kSize;
   };
-  auto row_step = [&](int r) { return R.reverse ? 31 - r : r; };
+  auto row_step = [&](int r) { return reverse ? 31 - r : r; };
 
   // one tile: blocks of 1 KiB dealt to the waves, block i VB + wave. A lane fills one chunk of one row
   // of its block, that is, fetches the one which the permutation puts there; its offset is the same
@@ -450,7 +459,7 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
     constexpr uint32_t kChunks = Tile::kLine / 16;
     const uint32_t row = static_cast<uint32_t>(lane) / kChunks;
     const uint32_t c = (static_cast<uint32_t>(lane) % kChunks) ^ Tile::permute(row + static_cast<uint32_t>(odd) * Tile::kRows);
-    return static_cast<uint32_t>(R.reverse ? Tile::kRows - 1 - row : row) * static_cast<uint32_t>(v.st * kSize) + c * 16u;
+    return static_cast<uint32_t>(reverse ? Tile::kRows - 1 - row : row) * static_cast<uint32_t>(v.st * kSize) + c * 16u;
   };
   const lin_type<TileK> tile_k{};
   const lin_type<TileV> tile_v{};
@@ -469,22 +478,23 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
     base_q = at_first(R.q);
     turn_q = static_cast<i64>(turn) * R.q.st * kSize;
   }
+  const uint32_t step_k = lin_kept(static_cast<uint32_t>(R.k.st * kSize)), step_v = lin_kept(static_cast<uint32_t>(R.v.st * kSize));
+  const uint32_t step_q = kFull ? lin_kept(static_cast<uint32_t>(R.q.st * kSize)) : 0;
   // `rows`: the chunk's steps (fewer than 32 in a segment's last one)
-  auto fetch = [&](const char* base, const LinView& v, const uint32_t (&off)[kOdd], int rows, int width, lds_bytes dst, auto tile) {
+  auto fetch = [&](const char* base, uint32_t step_bytes, const uint32_t (&off)[kOdd], int rows, int width, lds_bytes dst, auto tile) {
     typedef typename decltype(tile)::type Tile;
     constexpr uint32_t kChunks = Tile::kLine / 16;
     const rsrc_t r = lin_rsrc(base);
-    const uint32_t step_bytes = static_cast<uint32_t>(v.st * kSize);
-    const bool plain = rows >= 32 && width * kSize * 32 == Tile::kBytes;
+    const bool checked = rarely(rows < 32 || width * kSize * 32 != Tile::kBytes);
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
-      if (plain != (pass == 0)) continue;
+      if (checked != (pass == 1)) continue;
 #pragma unroll
       for (int i = 0; i < (Tile::kBlocks + VB - 1) / VB; ++i) {
         const int blk = i * VB + wave;
         if (Tile::kBlocks % VB != 0 && blk >= Tile::kBlocks) break;
         const int group = blk / Tile::kBlocksInGroup, part = blk % Tile::kBlocksInGroup;
-        const uint32_t shift = static_cast<uint32_t>(R.reverse ? Tile::kBlocksInGroup - 1 - part : part) * Tile::kRows * step_bytes +
+        const uint32_t shift = static_cast<uint32_t>(reverse ? Tile::kBlocksInGroup - 1 - part : part) * Tile::kRows * step_bytes +
                                static_cast<uint32_t>(group * Tile::kLine);
         uint32_t o = off[i & (kOdd - 1)];
         if (pass == 1) {
@@ -498,23 +508,23 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
     }
   };
   auto issue = [&](lds_bytes stg, int rows) {
-    fetch(base_k, R.k, off_k, rows, KD, stg, tile_k);
-    fetch(base_v, R.v, off_v, rows, VD, stg + kTileK, tile_v);
+    fetch(base_k, step_k, off_k, rows, KD, stg, tile_k);
+    fetch(base_v, step_v, off_v, rows, VD, stg + kTileK, tile_v);
     base_k += turn_k;
     base_v += turn_v;
     if constexpr (kFull) {
-      fetch(base_q, R.q, off_q, rows, KD, stg + kTileK + kTileV, tile_k);
+      fetch(base_q, step_q, off_q, rows, KD, stg + kTileK + kTileV, tile_k);
       base_q += turn_q;
     }
   };
   // log decay entering position p0 + li, 0 past the end; backward in time that of the step after it
   // (0 at the first position)
   const float* gate = a.gate + it.row * a.gate_b + it.start * a.gate_t + it.head * a.gate_h;
-  const char* base_g = reinterpret_cast<const char*>(gate + (static_cast<i64>(low) + (R.reverse ? 1 : 0)) * a.gate_t);
+  const char* base_g = reinterpret_cast<const char*>(gate + (static_cast<i64>(low) + (reverse ? 1 : 0)) * a.gate_t);
   const i64 turn_g = static_cast<i64>(turn) * a.gate_t * 4;
   const uint32_t off_g = static_cast<uint32_t>(row_step(static_cast<int>(li))) * static_cast<uint32_t>(a.gate_t * 4);
   auto load_gate = [&](int p0) -> float {
-    const bool in = p0 + static_cast<int>(li) < p_end && !(R.reverse && p0 + static_cast<int>(li) == 0);
+    const bool in = p0 + static_cast<int>(li) < p_end && !(reverse && p0 + static_cast<int>(li) == 0);
     const float g = buf_ld(lin_rsrc(base_g), in ? off_g : kLinOutside, 0);
     base_g += turn_g;
     return g;
@@ -591,7 +601,7 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < VB; ++w) s += dots[(p0 >> 5) & 1][w][lane];
-    dot_row[R.reverse ? it.len - 1 - p0 - lane : p0 + lane] = s;
+    dot_row[reverse ? it.len - 1 - p0 - lane : p0 + lane] = s;
   };
 
   // A chunk is one run of steps as a rule. A run ends before a step whose decays since the run's
@@ -625,7 +635,7 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
       }
       const bool odd = __ballot(!(top.v < kTame)) != 0;
       uint32_t odds = 0;
-      if (odd) {
+      if (rarely(odd)) {
 #pragma unroll 1
         for (int s = 0; s < 2; ++s) {
           const f32x8 v = Ops::widen(s == 0 ? vt[0] : vt[1]);
@@ -645,7 +655,7 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
       const float g_first = lane_value(g2, first);
       const bool drop = ((resets >> first) & 1u) != 0;
       E += static_cast<double>(g_first);
-      if (drop || !(fabs(E) <= static_cast<double>(kMild)) || ((odds >> first) & 1u) != 0) {
+      if (rarely(drop || !(fabs(E) <= static_cast<double>(kMild)) || ((odds >> first) & 1u) != 0)) {
         const float f = power(E);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
@@ -653,7 +663,7 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
           for (int r = 0; r < 16; ++r) S[kb][r] = drop ? 0.0f : S[kb][r] * f;
         E = 0.0;
       }
-      if (odd) {  // what is not finite must not meet a factor of zero
+      if (rarely(odd)) {  // what is not finite must not meet a factor of zero
 #pragma unroll
         for (int s = 0; s < 2; ++s) vt[s] = Ops::keep(vt[s], run >> (16 * s + 8 * half));
       }
@@ -701,19 +711,30 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
       // ---- the state after the run, and + sum_{j <= i} (q_i . k_j) v'_j: the first half of the
       // state's products runs while the scores are rounded, the second while those of the outputs end
       const bool part = last - first != 32;
+      typename Ops::raw kt[2];  // k^T of a block of 32 columns, read while the one before it is used
+      auto read_block = [&](int kb) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) kt[s] = Ops::template column_slice<TileK>(tk, kb, lane, s);
+      };
       auto state_products = [&](int from, int to) {
 #pragma unroll
-        for (int s = from; s < to; ++s) {
-          typename Ops::raw raw_kt = Ops::template column_slice<TileK>(tk, s >> 1, lane, s & 1);
-          if (part) {  // other steps' k are cleared, whatever they hold
+        for (int kb = from; kb < to; ++kb) {
+          typename Ops::raw now[2] = {kt[0], kt[1]};
+          if (kb + 1 < KB) read_block(kb + 1);
+          if (rarely(part)) {  // other steps' k are cleared, whatever they hold
             asm volatile("");  // (a branch, not masks for every chunk)
-            raw_kt = Ops::keep(raw_kt, run >> (16 * (s & 1) + 8 * half));
-          }
-          const frag kt = Ops::operand(raw_kt);
 #pragma unroll
-          for (int n = NV - 1; n >= 0; --n) S[s >> 1] = Ops::mma(kt, vw[s & 1][n], S[s >> 1]);
+            for (int s = 0; s < 2; ++s) now[s] = Ops::keep(now[s], run >> (16 * s + 8 * half));
+          }
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const frag f = Ops::operand(now[s]);
+#pragma unroll
+            for (int n = NV - 1; n >= 0; --n) S[kb] = Ops::mma(f, vw[s][n], S[kb]);
+          }
         }
       };
+      read_block(0);
       if constexpr (kFull) {
         // scores of the run's steps up to i; others may be infinite or NaN: one term is cleared as
         // it is, several before they are formed, for a pair's values meet in them
@@ -727,7 +748,7 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
             Ops::template split<NP>(pv, pf[s]);
             pf[s][0] = lin_masked(pf[s][0], earlier[s]);
           }
-          if (part) {
+          if (rarely(part)) {
             asm volatile("");
 #pragma unroll
             for (int s = 0; s < 2; ++s) pf[s][0] = lin_masked(pf[s][0], lin_mask(run >> (16 * s + 8 * half)));
@@ -742,7 +763,7 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
             Ops::template split<NP>(pv, pf[s]);
           }
         }
-        state_products(0, kSlices / 2);
+        state_products(0, KB / 2);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           // products of terms down to 2^-24 of the whole, of a score of one term to 2^-16
@@ -753,9 +774,9 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
             for (int m = NP - 1; m >= 0; --m)
               if (n + m < kTerms) O = Ops::mma(vw[s][n], pf[s][m], O);
         }
-        state_products(kSlices / 2, kSlices);
+        state_products(KB / 2, KB);
       } else {
-        state_products(0, kSlices);
+        state_products(0, KB);
       }
       if constexpr (kFull) {
         const float e_i = __builtin_ldexpf(__builtin_amdgcn_exp2f(x), n_E) * o_scale;
@@ -785,7 +806,7 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
       E += static_cast<double>(d_last);
       seg_decay = drop ? 0.0f : seg_decay * __builtin_amdgcn_exp2f(g_first + d_last);
       first = last;
-    } while (first < 32);
+    } while (rarely(first < 32));
     if constexpr (kFull) base_o += turn_o;
   };
 
