@@ -549,7 +549,7 @@ size_t slstm_linear_attention_backward_workspace_bytes(int B, int T, int n_heads
  *              is not trained)
  *  dstate0     as state0, NULL skips it
  * With dlog_decay the products keep float32 precision (it is a sum whose terms cancel), without it
- * that of the bf16 outputs. The workspace is always needed.
+ * that of the bf16 outputs. The workspace is always needed. Outputs must not alias inputs.
  */
 slstm_status slstm_linear_attention_backward(const slstm_heads* q, const slstm_heads* k,
                                              const slstm_heads* v, slstm_dtype dtype,

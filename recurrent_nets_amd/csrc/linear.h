@@ -36,15 +36,21 @@
 // Operands with the step index along the registers (k^T, v^T) are read by the transposing LDS load
 // (bf16) or element by element (float32).
 //
-// Tiles of q, k and v are copied global to LDS directly, a stage ahead, one barrier a chunk. LDS
-// rows lie in lines of 128 bytes; their 16-byte chunks are permuted by row (LinTile) so that
-// the 16 rows (or 4 rows by 32 bytes) that the LDS serves together lie on distinct banks. Steps
-// past the end and columns past the width are fetched from outside the buffer's extent: zeros.
+// Tiles of q, k and v are copied global to LDS directly, a chunk ahead, one barrier a chunk. LDS
+// rows lie in lines of 128 bytes; their 16-byte chunks are permuted by row (LinTile) so that the 16
+// rows (or 4 rows by 64 bytes) that the LDS serves together lie on distinct banks. Steps past the
+// end and columns past the width are fetched from outside the buffer's extent: zeros.
 //
-// Precision. bf16 operands are exact; products accumulate in float32 and the state is float32.
-// What has to be rounded to feed a bf16 product (scores, the scaled values, the state as an
-// operand) is split into NP, NV and NS bf16 terms, 8 bits of the mantissa each. float32 operands
-// use the float32 matrix instructions, with no rounding.
+// Precision. Products accumulate in float32, the state is float32 and its exponent E float64. bf16
+// operands are exact; what has to be rounded to feed a product (scores, the scaled values, the state
+// as an operand) is split into NP, NV and NS bf16 terms, 8 bits of the mantissa each (the kernel says
+// how many and why). float32 operands are split into three terms, float32's 24 bits.
+//
+// Bound by HBM where there are walks enough: 128 x 2048 steps, 8 heads of 128, bf16, take 0.51 ms,
+// 4.5 TB/s (loads without products run at 5.0); 4 x 16384 steps, 16 heads, 0.39 ms, of which the
+// segments' own states 0.14. The exact roles of the backward are bound by issue: a chunk has 68 matrix
+// and about 500 vector instructions a wave (16 x 4096 steps, 8 heads of 128: 0.59 ms a call). Short
+// walks are bound by a chunk's dependent steps, about 2.5 us alone on a compute unit.
 //
 // Causality holds for what is not finite too: scores of later steps are cleared, not multiplied by
 // zero, and a step with a v that is infinite or NaN begins a run, so that no earlier row of its
@@ -535,8 +541,11 @@ __device__ __forceinline__ void linear_walk(const LinLaunch& a, const LinRole& R
   f32x16 S[KB];
   const float* from = nullptr;
   int rs = VD, cs = 1;
-  if (kFull && it.seg > 0) {
-    from = R.seg_states + (static_cast<i64>(it.slot - 1) * a.H + it.head) * KD * VD;
+  if (kFull && (it.seg > 0 || p_end < it.len)) {
+    // a later segment's start, from the join; the first one's is with the last segment, so that the
+    // state given is not read here, where another workgroup may be writing the final state over it
+    const int slot = it.seg > 0 ? it.slot - 1 : it.slot + (it.len + a.seg_len - 1) / a.seg_len - 1;
+    from = R.seg_states + (static_cast<i64>(slot) * a.H + it.head) * KD * VD;
   } else if (kFull && R.state_in != nullptr) {
     from = R.state_in + (static_cast<i64>(it.seq) * a.H + it.head) * KD * VD;
     if (R.transposed) rs = 1, cs = KD;

@@ -296,14 +296,15 @@ def test_no_steps(amd):
     assert o.shape == v.shape and torch.equal(S, s0) and dg.shape == g.shape and torch.equal(ds, s0)
 
 
-def test_continued_prompt_in_place(amd):
-    """A prompt in two parts, the state passed on in its own buffer."""
-    p = Problem(29, 2, 150, 2, 32, 32, "f32")
+@pytest.mark.parametrize("T,cut", [(150, 61), (1500, 700)])
+def test_continued_prompt_in_place(amd, T, cut):
+    """A prompt in two parts, the state passed on in its own buffer, also in segments of time."""
+    p = Problem(29, 2, T, 2, 32, 32, "f32")
     case("linear attention continued")
     whole, S = p.check_forward(amd)
     state = p.s0.clone()
     parts = []
-    for sl in (slice(0, 61), slice(61, 150)):
+    for sl in (slice(0, cut), slice(cut, T)):
         o, _ = amd.linear_attention_forward(p.q[:, sl], p.k[:, sl], p.v[:, sl], p.g[:, sl].contiguous(), state, scale=p.scale,
                                             final_state=state)
         parts.append(o)
